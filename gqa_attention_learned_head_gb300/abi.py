@@ -13,6 +13,13 @@ ERR_BAD_PAGE = 4
 ERR_TIMEOUT = 5
 ERR_CUDA = 6
 ERR_BAD_LENGTH = 7
+ERR_NO_PAGES = 8
+ERR_BAD_VALUE = 9
+ERR_BAD_INDEX = 10
+
+DTYPE_F32 = 0
+DTYPE_BF16 = 1
+DTYPE_F16 = 2
 
 
 class DecodeDims(ctypes.Structure):
@@ -45,9 +52,32 @@ class MergeDims(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("num_splits", "num_rows", "num_heads", "head_dim")]
 
 
+class BeamDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_groups", "num_beams", "vocab", "num_select", "dtype", "pad_token")]
+    _fields_ += [("row_stride", ctypes.c_int64)]
+
+
+class ForkDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_rows_in", "num_rows_out", "num_pages", "max_pages", "page_size",
+                                              "grow")]
+
+
+class MoveDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_layers", "num_rows", "num_kv_heads", "head_dim", "page_size",
+                                              "num_pages", "max_pages", "max_accepted")]
+
+
+class BeamsDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_groups", "num_beams", "num_q_heads", "num_kv_heads", "head_dim",
+                                              "page_size", "num_pages", "max_pages", "num_workers")]
+
+
 EXPORTS = ("sinkattn_decode", "sinkattn_prefill", "sinkattn_merge", "sinkattn_decode_workspace_size", "sinkattn_verify",
            "sinkattn_verify_workspace_size", "sinkattn_kv_append", "sinkattn_prefill_paged", "sinkattn_verify_tree", "sinkattn_qkv_prologue",
-           "sinkattn_get_error", "sinkattn_status_string", "sinkattn_version", "sinkattn_selftest_wait_timeout")
+           "sinkattn_get_error", "sinkattn_status_string", "sinkattn_version", "sinkattn_selftest_wait_timeout",
+           "sinkattn_beam_select", "sinkattn_beam_select_workspace_size", "sinkattn_pages_fork",
+           "sinkattn_pages_fork_workspace_size", "sinkattn_kv_copy", "sinkattn_kv_compact", "sinkattn_decode_beams",
+           "sinkattn_decode_beams_workspace_size")
 
 
 def declare(lib):
@@ -68,6 +98,17 @@ def declare(lib):
     lib.sinkattn_qkv_prologue.argtypes = [P, P, P, P, P, ctypes.POINTER(RopeParams), P, P, P,
                                           ctypes.POINTER(PagedDims), P]
     lib.sinkattn_prefill_paged.argtypes = [P, P, P, P, P, P, P, f32, P, P, ctypes.POINTER(PagedDims), P]
+    lib.sinkattn_beam_select.argtypes = [P, P, P, P, P, P, ctypes.POINTER(BeamDims), P, sz, P]
+    lib.sinkattn_beam_select_workspace_size.argtypes = [ctypes.POINTER(BeamDims)]
+    lib.sinkattn_beam_select_workspace_size.restype = sz
+    lib.sinkattn_pages_fork.argtypes = [P, P, P, P, P, P, P, P, P, P, ctypes.POINTER(ForkDims), P, sz, P]
+    lib.sinkattn_pages_fork_workspace_size.argtypes = [ctypes.POINTER(ForkDims)]
+    lib.sinkattn_pages_fork_workspace_size.restype = sz
+    lib.sinkattn_kv_copy.argtypes = [P, P, P, ctypes.POINTER(MoveDims), P]
+    lib.sinkattn_kv_compact.argtypes = [P, P, P, P, P, P, ctypes.POINTER(MoveDims), P]
+    lib.sinkattn_decode_beams.argtypes = [P, P, P, P, P, P, f32, P, P, ctypes.POINTER(BeamsDims), P, sz, P]
+    lib.sinkattn_decode_beams_workspace_size.argtypes = [ctypes.POINTER(BeamsDims)]
+    lib.sinkattn_decode_beams_workspace_size.restype = sz
     lib.sinkattn_get_error.argtypes = [P]
     lib.sinkattn_selftest_wait_timeout.argtypes = [P]
     lib.sinkattn_selftest_wait_timeout.restype = ctypes.c_int
@@ -75,7 +116,9 @@ def declare(lib):
     lib.sinkattn_status_string.restype = ctypes.c_char_p
     lib.sinkattn_version.restype = i32
     for fn in ("sinkattn_decode", "sinkattn_prefill", "sinkattn_merge", "sinkattn_get_error", "sinkattn_verify",
-               "sinkattn_kv_append", "sinkattn_prefill_paged", "sinkattn_verify_tree", "sinkattn_qkv_prologue"):
+               "sinkattn_kv_append", "sinkattn_prefill_paged", "sinkattn_verify_tree", "sinkattn_qkv_prologue",
+               "sinkattn_beam_select", "sinkattn_pages_fork", "sinkattn_kv_copy", "sinkattn_kv_compact",
+               "sinkattn_decode_beams"):
         getattr(lib, fn).restype = ctypes.c_int
     return lib
 

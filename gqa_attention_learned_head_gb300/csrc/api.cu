@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "call_range.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace sinkattn {
@@ -25,11 +26,6 @@ __global__ void take_error_kernel(unsigned* err, unsigned* taken) { *taken = ato
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceState {
-    bool ready = false;
-    unsigned* err = nullptr;    // device address of g_error_word
-    unsigned* taken = nullptr;  // device address of g_error_taken
-};
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
 
@@ -37,6 +33,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
+
+}  // namespace
 
 sinkattn_status_t device_state(DeviceState** out) {
     int dev = 0;
@@ -64,7 +62,7 @@ sinkattn_status_t device_state(DeviceState** out) {
     return SINKATTN_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+namespace {
 
 // A bf16, 128-byte-swizzled tensor map of `rank` dimensions (the innermost one 64 elements of
 // 128 B), encoded once per distinct (base, dims, strides, box) in each host thread: a serving loop
@@ -113,6 +111,8 @@ bool encode_cached(CUtensorMap* map, int rank, const void* base, const cuuint64_
     return true;
 }
 
+}  // namespace
+
 // 3-D map over q [tokens, H, 64] whose box is 64 x box_heads heads x box_tokens tokens (the rows of
 // one query-head group of several consecutive tokens).
 bool encode_token_groups(CUtensorMap* map, const void* base, long long tokens, int H, unsigned box_heads,
@@ -131,6 +131,8 @@ bool encode_rows(CUtensorMap* map, const void* base, unsigned long long rows, un
     const cuuint32_t box[2] = {64, box_rows};
     return encode_cached(map, 2, base, dims, strides, box);
 }
+
+namespace {
 
 // 3-D map over [T, H, 64] (token-major), box = box_rows tokens x 1 head x 64.
 bool encode_thd(CUtensorMap* map, const void* base, int T, int H, unsigned box_rows) {
@@ -198,6 +200,9 @@ const char* sinkattn_status_string(sinkattn_status_t s) {
         case SINKATTN_ERR_TIMEOUT: return "device pipeline wait timed out";
         case SINKATTN_ERR_CUDA: return "CUDA runtime error";
         case SINKATTN_ERR_BAD_LENGTH: return "sequence length out of range";
+        case SINKATTN_ERR_NO_PAGES: return "not enough free pages";
+        case SINKATTN_ERR_BAD_VALUE: return "NaN or +infinity where a finite value is needed";
+        case SINKATTN_ERR_BAD_INDEX: return "row or token index out of range";
     }
     return "unknown status";
 }

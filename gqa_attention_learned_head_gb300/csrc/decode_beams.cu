@@ -1,0 +1,801 @@
+// decode_beams.cu -- decode of groups of rows (beams, or samples of one prompt) whose page tables share
+// pages, on the fifth-generation tensor cores.
+//
+// The attention is the sink attention of "GPT-OSS on day 0" (Perplexity), section "Kernels for GPT-OSS / Sink
+// Attention", of one query token per row over the row's own pages; the posts describe no sharing of pages
+// between rows.  Softmax over a row's keys can be summed in any order and in any pieces, so the pages of a group
+// are taken not row by row but once each: every distinct (column, page) with the set of rows that hold it.
+//
+// GB300 design.  beams_plan_kernel lists each group's distinct pages (8 columns' worth of a K x max_pages table
+// to the microsecond: latency); decode_beams_kernel, its programmatic dependent, streams them.  The R = K x G
+// query rows of one (group n, KV head g) -- row r = k * G + h is row k's query head g * G + h -- form ONE tcgen05
+// tile (R <= 128, padded to the MMA's 128 rows), so a page is read once for all rows and every product runs on
+// the tensor core; a row's keys are masked by the page's row set and the row's own length.
+// Work: the flattened list of (group, KV head, 8 distinct pages = 128 keys) units, one contiguous share per CTA
+// (one CTA per resident slot), cut at segment ends into pieces (the split of split_kv.cuh with tiles as units).
+// The pipeline runs on across the pieces of a share:
+//   warps 0, 3  TMA producers: warp 0 loads each piece's Q rows with one 3-D copy (64 dims x G heads x K rows,
+//               landing as rows k * G + h) into a 2-slot Q ring and the K tiles, warp 3 the V tiles; a tile is 8
+//               page copies of 2 KB (lanes 0-7), 128-byte swizzle.
+//   warp 1      allocates 256 TMEM columns; issues S_j = Q K_j^T.
+//   warp 2      issues O += P_j V_j (P read from TMEM; the first tile of a piece starts O afresh).
+//   warps 4-7   softmax, thread r = row r (only the warps that hold rows work); at a piece's end they read O and
+//               write the rows (or fp32 partials).
+// The piece with a segment's first tile is seeded with the sink.  The pieces of a segment split between CTAs
+// write fp32 partials; the CTA holding the segment's first piece lists it, and the split-merge kernel, launched
+// right behind this one as a programmatic dependent, combines them.  Every wait is bounded.
+#include "args_beams.h"
+#include "args_merge.h"
+#include "ptx.cuh"
+#include "split_kv.cuh"
+#include "tc_tile.cuh"
+
+#include <cooperative_groups.h>
+
+namespace cg = cooperative_groups;
+
+namespace sinkattn {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 256;
+constexpr uint32_t kTmemCols = 256;
+constexpr uint32_t kColS = 0, kColO = 128, kColP = 192;
+constexpr int kKStages = 2, kVStages = 2;
+constexpr int kPagesPerTile = kBN / kPageSize;  // 8
+constexpr int kMinTiles = kBeamsMinTiles;  // automatic mode: never cut shares finer than this
+
+constexpr int kPlanThreads = 256;
+
+// Lists the distinct pages of group blockIdx.x / ctas, by column and, within one, by the first row that holds
+// them.  Each of the group's `ctas` CTAs (a cluster) takes a contiguous run of columns, a thread one column at a
+// time; with more than one CTA the columns are counted first, so that each knows where its entries start.
+template <int KMAX>
+__global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArgs a) {
+    __shared__ int len[kBeamsMaxBeams];
+    __shared__ int red[kPlanThreads / 32];
+    __shared__ int counted;
+    cg::cluster_group cluster = cg::this_cluster();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K, cap = a.max_pages * kPageSize;
+    const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), n = (int)(blockIdx.x / (unsigned)ctas);
+    if (tid < K) {
+        const int raw = __ldcg(&a.kv_lens[(long long)n * K + tid]);
+        if ((raw < 0 || raw > cap) && rank == 0) atomicOr(a.err, kErrBadLength);
+        len[tid] = clamp_len(raw, cap);
+    }
+    __syncthreads();
+    int longest = 0, shortest = cap;
+    for (int k = 0; k < K; ++k) {
+        longest = max(longest, len[k]);
+        shortest = min(shortest, len[k]);
+    }
+    const int cols = (longest + kPageSize - 1) / kPageSize;
+    const int per = (cols + ctas - 1) / ctas, c0 = min(cols, rank * per), c1 = min(cols, c0 + per);
+    const int* table = a.page_table + (long long)n * K * a.max_pages;
+
+    int id[KMAX];       // the column's page of each row, -1 where it has none
+    unsigned set[KMAX]; // the rows that hold the same page, for the first of them; else 0
+    auto column = [&](int c, bool report) {
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k) {
+            id[k] = -1;
+            if (k < K && c < c1 && c * kPageSize < len[k]) {
+                const int page = __ldcg(&table[(long long)k * a.max_pages + c]);
+                if (page >= 0 && page < a.num_pages) id[k] = page;
+                else if (report) atomicOr(a.err, kErrBadPage);
+            }
+        }
+        int distinct = 0;
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k) {
+            unsigned same = 0;
+#pragma unroll
+            for (int j = 0; j < KMAX; ++j) same |= (id[j] == id[k]) ? 1u << j : 0u;
+            set[k] = (id[k] >= 0 && __ffs(same) - 1 == k) ? same : 0u;
+            distinct += set[k] != 0u;
+        }
+        return distinct;
+    };
+    auto block_sum = [&](int v, int& total) {  // exclusive prefix of v over the CTA's threads
+        int incl = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) red[warp] = incl;
+        __syncthreads();
+        int before = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            before += w < warp ? red[w] : 0;
+            total += red[w];
+        }
+        return before + incl - v;
+    };
+
+    int at = 0, total;
+    if (ctas > 1) {
+        int mine = 0;
+        for (int c = c0 + tid; c < c1; c += kPlanThreads) mine += column(c, false);
+        (void)block_sum(mine, total);
+        if (tid == 0) counted = total;
+        cluster.sync();
+        for (int i = 0; i < rank; ++i) at += *cluster.map_shared_rank(&counted, i);
+        cluster.sync();  // no CTA ends while another reads its count
+    }
+    PageEntry* out = a.entries + (long long)n * K * a.max_pages;
+    for (int base = c0; base < c1; base += kPlanThreads) {
+        const int c = base + tid, distinct = column(c, true);
+        int to = at + block_sum(distinct, total);
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k) {
+            if (!set[k]) continue;
+            int slots = 0;
+#pragma unroll
+            for (int j = 0; j < KMAX; ++j)
+                if ((set[k] >> j) & 1u) slots = max(slots, min(kPageSize, len[j] - c * kPageSize));
+            const bool all = __popc(set[k]) == K && shortest >= (c + 1) * kPageSize;
+            *reinterpret_cast<int4*>(out + to++) = make_int4(id[k], c, (int)set[k], slots | (all ? kAllSee : 0));
+        }
+        at += total;
+    }
+    if (rank == ctas - 1 && tid == 0) a.counts[n] = at;
+}
+
+// What the plan kernel wrote is read through L2 (ld.cg): this kernel may be resident before it has been written.
+__device__ __forceinline__ int count_of(const BeamsArgs& a, int n) { return __ldcg(&a.counts[n]); }
+__device__ __forceinline__ int tiles_of(int pages) { return (pages + kPagesPerTile - 1) / kPagesPerTile; }
+__device__ __forceinline__ PageEntry entry_of(const BeamsArgs& a, int n, int i) {
+    const int4 e = __ldcg(reinterpret_cast<const int4*>(a.entries + (long long)n * a.K * a.max_pages + i));
+    return PageEntry{e.x, e.y, (unsigned)e.z, e.w};
+}
+
+// One piece: tiles [ta, tb) of segment (b, g) (group b), whose first unit is seg_start and which has `tiles`
+// tiles and `pages` distinct pages.
+struct Piece {
+    int b, g, ta, tb, tiles, pages;
+    long long seg_start;
+};
+
+// Walks the pieces of units [x, x1); every role of the CTA runs its own walker over the same share.
+struct Walk {
+    int b, g, tiles, pages;
+    long long seg_start, x, x1;
+    int B, Hkv;
+
+    // the next segment with at least one tile (a walk never passes the share's end)
+    __device__ void advance(const BeamsArgs& a) {
+        seg_start += tiles;
+        if (++g == Hkv) {
+            g = 0;
+            do {
+                ++b;
+                pages = count_of(a, b);
+                tiles = tiles_of(pages);
+            } while (tiles == 0 && b + 1 < B);
+        }
+    }
+    __device__ bool next(const BeamsArgs& a, Piece& p) {
+        if (x >= x1) return false;
+        while (x >= seg_start + tiles) advance(a);
+        p.b = b;
+        p.g = g;
+        p.tiles = tiles;
+        p.pages = pages;
+        p.seg_start = seg_start;
+        p.ta = (int)(x - seg_start);
+        const long long end = x1 < seg_start + tiles ? x1 : seg_start + tiles;
+        p.tb = (int)(end - seg_start);
+        x = end;
+        return true;
+    }
+};
+
+struct __align__(1024) Smem {
+    uint8_t q[2][kTileBytes];
+    uint8_t k[kKStages][kTileBytes];
+    uint8_t v[kVStages][kTileBytes];
+    uint64_t q_full[2], q_empty[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+    uint64_t s_full, s_free, p_full, o_done, mma_done;
+    uint32_t tmem_base;
+    long long red[8];    // block reductions
+    long long found[4];  // share start: group, its first unit, its tiles, flag
+    Walk walk[4];        // the softmax warps' walkers (kept out of their registers)
+    Piece piece[4];      // ... and their current pieces
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+    decode_beams_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const BeamsArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int B = a.N, Hkv = a.Hkv, R = a.R, K = a.K, G = a.G;
+    const int active = (R + 31) / 32;  // softmax warps that hold rows
+
+    // ---- 0. set-up that reads no input (barriers, tensor memory, the Q padding): done before the wait
+    // below, so it overlaps the preceding kernel's tail
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.q_full[i], 1);
+            mbar_init(&sm.q_empty[i], 1);
+        }
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(&sm.k_full[i], 1);
+            mbar_init(&sm.k_empty[i], 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(&sm.v_full[i], 1);
+            mbar_init(&sm.v_empty[i], 1);
+        }
+        mbar_init(&sm.s_full, 1);
+        mbar_init(&sm.s_free, 32 * active);
+        mbar_init(&sm.p_full, 32 * active);
+        mbar_init(&sm.o_done, 1);
+        mbar_init(&sm.mma_done, 2);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sm.tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    // Q rows R..127 (no query) are zeros, so their scores stay finite; the TMA writes rows 0..R-1
+    for (int e = R * 8 + tid; e < kBM * 8; e += kThreads) {
+        reinterpret_cast<uint4*>(sm.q[0])[e] = make_uint4(0u, 0u, 0u, 0u);
+        reinterpret_cast<uint4*>(sm.q[1])[e] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    fence_proxy_async_smem();
+
+    // a programmatic dependent of what precedes it on the stream: no input is read before that has
+    // completed; the split merge behind this kernel may be scheduled once every CTA runs
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- 1. units (Hkv x tiles) per group: their total U and, by a running block-wide scan, the
+    // group holding this share's first unit (one pass when the batch fits the CTA's threads)
+    if (tid == 0) sm.found[3] = 0;
+    long long U = 0, base = 0, lo = 0, cnt = 0;
+    for (int p0 = 0; p0 < B; p0 += kThreads) {
+        const int i = p0 + tid;
+        int ti = 0;
+        if (i < B) {
+            ti = tiles_of(count_of(a, i));
+        }
+        const long long c = (long long)ti * Hkv;
+        long long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        __syncthreads();  // red[] is free
+        if (lane == 31) sm.red[warp] = incl;
+        __syncthreads();
+        long long woff = 0, total = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            woff += w < warp ? sm.red[w] : 0;
+            total += sm.red[w];
+        }
+        if (B <= kThreads) {  // one pass: this thread's request and its units stay in registers
+            lo = woff + incl - c;
+            cnt = c;
+        }
+        U = base + total;
+        base = U;
+    }
+    {  // rows of groups without a page carry only the sink
+        const long long rows = (long long)B * K * a.Hq;
+        for (long long r = (long long)blockIdx.x * kThreads + tid; r < rows; r += (long long)gridDim.x * kThreads) {
+            const int b = (int)(r / ((long long)K * a.Hq));
+            if (count_of(a, b) != 0) continue;
+            uint4* dst = reinterpret_cast<uint4*>(a.out + r * kHeadDim);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+            if (a.lse) a.lse[r] = __ldg(&a.sinks[r % a.Hq]);
+        }
+    }
+    const long long C = U > 0 ? effective_shares(a.tc_grid, a.fixed_workers, kMinTiles, U) : 0;
+    const long long cta = blockIdx.x;
+    if (cta >= C) {  // no share: release the tensor memory taken above (the whole CTA is here)
+        if (tid == 0 && a.merge_list) a.merge_list[cta] = make_int2(-1, 0);
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 1) {
+            tc_fence_after();
+            tmem_dealloc(sm.tmem_base, kTmemCols);
+        }
+        return;
+    }
+    const long long x0 = cta * U / C, x1 = (cta + 1) * U / C;
+    if (B <= kThreads) {
+        if (cnt > 0 && x0 >= lo && x0 < lo + cnt) {
+            sm.found[0] = tid;
+            sm.found[1] = lo;
+            sm.found[2] = cnt / Hkv;
+        }
+        __syncthreads();
+    } else {
+        // ---- 2. a second scan, now that U (and so x0) is known
+        base = 0;
+        for (int p0 = 0; p0 < B; p0 += kThreads) {
+            const int i = p0 + tid;
+            const int ti = i < B ? tiles_of(count_of(a, i)) : 0;
+            const long long c = (long long)ti * Hkv;
+            long long incl = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            __syncthreads();  // red[] (and found[3]) are settled
+            if (lane == 31) sm.red[warp] = incl;
+            __syncthreads();
+            long long woff = 0, total = 0;
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) {
+                woff += w < warp ? sm.red[w] : 0;
+                total += sm.red[w];
+            }
+            const long long l0 = base + woff + incl - c;
+            if (c > 0 && x0 >= l0 && x0 < l0 + c) {
+                sm.found[0] = i;
+                sm.found[1] = l0;
+                sm.found[2] = ti;
+                sm.found[3] = 1;
+            }
+            base += total;
+            __syncthreads();
+            if (sm.found[3]) break;
+        }
+    }
+    Walk walk;
+    walk.B = B;
+    walk.Hkv = Hkv;
+    walk.b = (int)sm.found[0];
+    walk.tiles = (int)sm.found[2];
+    walk.pages = count_of(a, walk.b);
+    walk.g = (int)((x0 - sm.found[1]) / walk.tiles);
+    walk.seg_start = sm.found[1] + (long long)walk.g * walk.tiles;
+    walk.x = x0;
+    walk.x1 = x1;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = sm.tmem_base;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0 || warp == 3) {
+            // ------------------------------------------------------------ TMA producers
+            const bool is_k = warp == 0;
+            const int stages = is_k ? kKStages : kVStages;
+            uint64_t* full = is_k ? sm.k_full : sm.v_full;
+            uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
+            const CUtensorMap* map = is_k ? &tmap_k : &tmap_v;
+            if (lane == 0) {
+                tma_prefetch_desc(map);
+                if (is_k) tma_prefetch_desc(&tmap_q);
+            }
+            int J = 0, p = 0, issued = 0;  // tiles, pieces (their Q issued) and tile copies issued so far
+            bool ok = true;
+            Piece pc;
+            while (ok && walk.next(a, pc)) {
+                if (is_k) {  // this piece's Q rows into Q slot p & 1, once the piece two back has used it
+                    int got = 1;
+                    if (lane == 0) {
+                        if (p >= 2) got = mbar_wait(&sm.q_empty[p & 1], ((p >> 1) - 1) & 1);
+                        if (got) {
+                            mbar_arrive_expect_tx(&sm.q_full[p & 1], (uint32_t)R * 128u);
+                            tma_load_3d(sm.q[p & 1], &tmap_q, 0, pc.g * G, pc.b * K, &sm.q_full[p & 1]);
+                        }
+                    }
+                    if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
+                }
+                ++p;
+                // page ids (lanes 0-7), read one tile ahead of the copies
+                auto page_of = [&](int t) {
+                    const int i = t * kPagesPerTile + (lane & 7);
+                    return i < pc.pages ? entry_of(a, pc.b, i).page : -1;
+                };
+                int page = page_of(pc.ta);
+                for (int t = pc.ta; ok && t < pc.tb; ++t, ++J) {
+                    const int st = J % stages;
+                    if (J >= stages) {
+                        int got = 0;
+                        if (lane == 0) got = mbar_wait(&empty[st], ((J / stages) - 1) & 1);
+                        if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
+                    }
+                    // a tile's missing pages are copied from behind the pool's end: zeros
+                    const int row = page < 0 ? a.num_pages * Hkv * kPageSize : (page * Hkv + pc.g) * kPageSize;
+                    if (t + 1 < pc.tb) page = page_of(t + 1);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[st], kTileBytes);
+                    __syncwarp();
+                    uint8_t* tile = is_k ? sm.k[st] : sm.v[st];
+                    if (lane < kPagesPerTile) tma_load_2d(tile + lane * (kPageSize * 128), map, 0, row, &full[st]);
+                    issued = J + 1;
+                }
+            }
+            if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
+            // every copy this warp started has landed before the CTA can exit (bounded)
+            if (lane == 0) {
+                for (int j = issued - stages < 0 ? 0 : issued - stages; j < issued; ++j)
+                    (void)mbar_wait(&full[j % stages], (j / stages) & 1);
+                if (is_k)
+                    for (int q = p - 2 < 0 ? 0 : p - 2; q < p; ++q) (void)mbar_wait(&sm.q_full[q & 1], (q >> 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ------------------------------------------------------------ S issuer: S_j = Q K_j^T
+            // (the whole warp walks the loop, one elected lane issues)
+            const uint32_t tS = tbase + kColS;
+            int J = 0, p = 0;
+            bool ok = true;
+            Piece pc;
+            while (ok && walk.next(a, pc)) {
+                if (!(ok = warp_wait(&sm.q_full[p & 1], (p >> 1) & 1))) break;
+                const uint32_t qaddr = smem_u32(sm.q[p & 1]);
+                for (int t = pc.ta; t < pc.tb; ++t, ++J) {
+                    const int st = J % kKStages;
+                    ok = warp_wait(&sm.k_full[st], (J / kKStages) & 1) && (J == 0 || warp_wait(&sm.s_free, (J - 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t kaddr = smem_u32(sm.k[st]);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_ss_warp(tS, sw128_desc(qaddr + kk * 32), sw128_desc(kaddr + kk * 32), kIdescQK, kk > 0);
+                    tc_commit_warp(&sm.s_full);
+                    tc_commit_warp(&sm.k_empty[st]);
+                }
+                tc_commit_warp(&sm.q_empty[p & 1]);  // this piece's Q slot is free once its products end
+                ++p;
+            }
+            if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
+            tc_commit_warp(&sm.mma_done);  // every MMA of both issuers has finished before TMEM is released
+            (void)warp_wait(&sm.mma_done, 0);
+        } else if (warp == 2) {
+            // ------------------------------------------------------------ PV issuer: O += P_j V_j
+            // One elected lane issues; the whole warp zeroes the slots of V that hold no token of any row (they
+            // may hold anything, and a 0 weight times NaN is NaN) before a tile's product.
+            const uint32_t tO = tbase + kColO, tP = tbase + kColP;
+            int J = 0;
+            bool ok = true;
+            Piece pc;
+            while (ok && walk.next(a, pc)) {
+                auto slots_of = [&](int t) {
+                    const int i = t * kPagesPerTile + (lane & 7);
+                    return i < pc.pages ? entry_of(a, pc.b, i).slots & ~kAllSee : kPageSize;  // missing: zeros already
+                };
+                int slots = slots_of(pc.ta);
+                for (int t = pc.ta; t < pc.tb; ++t, ++J) {
+                    const int st = J % kVStages;
+                    ok = warp_wait(&sm.v_full[st], (J / kVStages) & 1);
+                    if (!ok) break;
+                    uint32_t part = __ballot_sync(0xffffffffu, lane < kPagesPerTile && slots < kPageSize);
+                    if (part) {
+                        while (part) {
+                            const int pg = __ffs(part) - 1;
+                            part &= part - 1;
+                            const int n = __shfl_sync(0xffffffffu, slots, pg);
+                            for (int e = (pg * kPageSize + n) * 8 + lane; e < (pg + 1) * kPageSize * 8; e += 32)
+                                reinterpret_cast<uint4*>(sm.v[st])[e] = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (t + 1 < pc.tb) slots = slots_of(t + 1);
+                    if (!(ok = warp_wait(&sm.p_full, J & 1))) break;
+                    tc_fence_after();
+                    const uint32_t vaddr = smem_u32(sm.v[st]);
+                    // P_j is written only after the softmax has read the previous piece's O, so the first tile of
+                    // a piece may start O afresh
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        tc_mma_ts_warp(tO, tP + ks * 8, sw128_desc(vaddr + ks * 2048), kIdescPV,
+                                       (t > pc.ta || ks > 0) ? 1u : 0u);
+                    tc_commit_warp(&sm.v_empty[st]);
+                    tc_commit_warp(&sm.o_done);
+                }
+            }
+            if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
+            tc_commit_warp(&sm.mma_done);
+            (void)warp_wait(&sm.mma_done, 0);
+        }
+    } else {
+        // 128 x 56 + 128 x 200 = 256 x 128, the launch's registers
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int r = tid - 128;
+        const bool live = r < R;
+        const int i = live ? r / G : 0, h = live ? r % G : 0;
+        int2 head = make_int2(-1, 0);  // the share's last piece, if it starts a segment it does not end
+        if (warp - 4 < active) {
+            // ---------------------------------------------------------------- softmax
+            const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t tS = tbase + lane_off + kColS, tO = tbase + lane_off + kColO, tP = tbase + lane_off + kColP;
+            const float scale_log2 = a.scale_log2;
+            int J = 0;
+            bool ok = true;
+            const int sw = warp - 4;
+            if (lane == 0) sm.walk[sw] = walk;
+            __syncwarp();
+            while (ok) {
+                int has = 0;
+                __syncwarp();  // every lane is done with the previous piece
+                if (lane == 0) has = sm.walk[sw].next(a, sm.piece[sw]) ? 1 : 0;
+                if (!__shfl_sync(0xffffffffu, has, 0)) break;
+                __syncwarp();
+                const Piece& pc = sm.piece[sw];
+                // this row's cached tokens (the plan kernel reported lengths out of range)
+                const int len = live ? clamp_len(__ldcg(&a.kv_lens[(long long)pc.b * K + i]), a.max_pages * kPageSize) : 0;
+                const int ta = pc.ta, tb = pc.tb;
+                const bool seeded = ta == 0;
+                float m = (seeded && live) ? __ldg(&a.sinks[pc.g * G + h]) * kLog2e : kNegInf;
+                float d = (seeded && live) ? 1.f : 0.f;  // the sink's own e^(sink - m) = 1
+                // a tile's page entries (lanes 0-7), read one tile ahead
+                auto load_entry = [&](int t) {
+                    const int e = t * kPagesPerTile + (lane & 7);
+                    return e < pc.pages ? entry_of(a, pc.b, e) : PageEntry{-1, 0, 0u, 0};
+                };
+                PageEntry entry = load_entry(ta);
+                for (int t = ta; t < tb; ++t, ++J) {
+                    const bool masked = !__all_sync(0xffffffffu, (entry.slots & kAllSee) != 0);
+                    // this row's visible keys of the tile: of each page, the slots its length reaches
+                    uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                    if (masked) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            vis[w] = 0u;
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const uint32_t beams = __shfl_sync(0xffffffffu, entry.beams, 2 * w + half);
+                                const int n = len - kPageSize * __shfl_sync(0xffffffffu, entry.col, 2 * w + half);
+                                const uint32_t bits = n >= kPageSize ? 0xFFFFu : (n > 0 ? (1u << n) - 1u : 0u);
+                                if (live && ((beams >> i) & 1u)) vis[w] |= bits << (16 * half);
+                            }
+                        }
+                    }
+                    if (t + 1 < tb) entry = load_entry(t + 1);
+                    if (!(ok = warp_wait(&sm.s_full, J & 1))) break;
+                    tc_fence_after();
+                    float s[128];
+#pragma unroll
+                    for (int cc = 0; cc < 4; ++cc)
+                        tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[cc * 32]));
+                    tc_wait_ld();
+                    tc_fence_before();
+                    mbar_arrive(&sm.s_free);
+
+                    float mul = scale_log2;
+                    if (!(scale_log2 > 0.f)) {  // zero or negative scale: scale first, mask after
+#pragma unroll
+                        for (int cc = 0; cc < 128; ++cc) s[cc] *= scale_log2;
+                        mul = 1.f;
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int cc = 0; cc < 128; ++cc) s[cc] = ((vis[cc >> 5] >> (cc & 31)) & 1u) ? s[cc] : kNegInf;
+                    }
+                    float acc[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = fmax3(s[e], s[8 + e], s[16 + e]);
+#pragma unroll
+                    for (int cc = 24; cc < 120; cc += 16)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = fmax3(acc[e], s[cc + e], s[cc + 8 + e]);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], s[120 + e]);
+                    const float mx_raw =
+                        fmaxf(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], fmax3(acc[5], acc[6], acc[7])));
+                    const float mx = mx_raw == kNegInf ? kNegInf : mx_raw * mul;
+                    const float m_new = fmaxf(m, mx);
+                    const bool first = t == ta;  // O starts afresh with this piece
+                    float factor = 1.f;
+                    bool rescale_o = false;
+                    if (first || m_new > m + kRescaleThreshold) {
+                        factor = (m_new == kNegInf) ? 1.f : fast_exp2(m - m_new);
+                        rescale_o = !first;
+                        m = m_new;
+                        d *= factor;
+                    }
+                    const float neg_m = (m == kNegInf) ? 0.f : -m;
+                    const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(neg_m, neg_m);
+                    float2 sums[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                      make_float2(0.f, 0.f)};
+                    uint32_t pk[64];
+#pragma unroll
+                    for (int cc = 0; cc < 64; ++cc) {
+                        const float2 xx = ffma2(make_float2(s[2 * cc], s[2 * cc + 1]), mul2, negm2);
+                        const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+                        sums[cc & 3] = fadd2(sums[cc & 3], pp);
+                        pk[cc] = pack_bf16(pp.x, pp.y);
+                    }
+                    const float2 s01 = fadd2(fadd2(sums[0], sums[1]), fadd2(sums[2], sums[3]));
+                    d += s01.x + s01.y;
+                    if (!first) {  // P_{j-1} consumed and O_{j-1} final before P and O are touched
+                        if (!(ok = warp_wait(&sm.o_done, (J - 1) & 1))) break;
+                        tc_fence_after();
+                        if (__any_sync(0xffffffffu, rescale_o)) {
+#pragma unroll
+                            for (int cc = 0; cc < 2; ++cc) {
+                                uint32_t o[32];
+                                tmem_ld32(tO + cc * 32, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * factor);
+                                tmem_st32(tO + cc * 32, o);
+                            }
+                        }
+                    }
+                    tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+                    tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                    tc_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(&sm.p_full);
+                }
+                if (!ok) break;
+                // ---- end of the piece (the PV of its last tile has finished): O / d of this row
+                if (!(ok = warp_wait(&sm.o_done, (J - 1) & 1))) break;
+                tc_fence_after();
+                uint32_t o[64];
+                tmem_ld32(tO, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+                tmem_ld32(tO + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                tc_wait_ld();
+                tc_fence_before();
+                const bool whole = seeded && tb == pc.tiles;
+                const int seg = pc.b * Hkv + pc.g;
+                if (seeded && !whole) {
+                    long long c_first = 0;
+                    int pieces = 0;
+                    segment_pieces(pc.seg_start, pc.tiles, C, U, c_first, pieces);
+                    head = make_int2(seg, pieces);
+                }
+                if (live) {
+                    const float inv = d > 0.f ? 1.f / d : 0.f;
+                    const float l2 = d > 0.f ? m + log2f(d) : kNegInf;
+                    if (whole) {
+                        const long long row = ((long long)pc.b * K + i) * a.Hq + pc.g * G + h;
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kHeadDim);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            uint4 w;
+                            w.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
+                            w.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
+                            w.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
+                            w.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                            dst[e] = w;
+                        }
+                        if (a.lse) a.lse[row] = l2 * kLn2;
+                    } else {
+                        const long long slot = cta + seg;  // partial slot of this piece
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * R + r) * kHeadDim);
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            dst[e] = make_float4(__uint_as_float(o[4 * e + 0]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
+                                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
+                        a.part_lse[slot * R + r] = l2;
+                    }
+                }
+            }
+            if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
+        }
+        // ---- list the segment whose first piece this share holds without completing it (the
+        // split merge combines its partials once every CTA has finished)
+        if (tid == 128 && a.merge_list) a.merge_list[cta] = head;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, kTmemCols);
+    }
+}
+
+}  // namespace
+
+// CTAs of the attention kernel that fit on one SM, from its registers, its shared memory (with the per-block
+// reservation) and its tensor memory (512 columns per SM, kTmemCols per CTA); the runtime's occupancy query
+// reports one for a kernel that allocates tensor memory, while the hardware keeps two resident.
+static cudaError_t beams_occupancy(int* per_sm, int* sms) {
+    static thread_local int cached[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    if (dev < 64 && cached[dev] > 0) {
+        *per_sm = cached[dev];
+        return cudaSuccess;
+    }
+    const size_t smem = 1024 + sizeof(Smem);
+    e = cudaFuncSetAttribute(decode_beams_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, decode_beams_kernel)) != cudaSuccess) return e;
+    int smem_sm = 0, reserved = 0, regs_sm = 0;
+    if ((e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&regs_sm, cudaDevAttrMaxRegistersPerMultiprocessor, dev)) != cudaSuccess)
+        return e;
+    const int regs_warp = ((fa.numRegs * 32 + 255) / 256) * 256;  // allocated per warp in units of 256
+    int n = 512 / (int)kTmemCols;
+    const int by_smem = (int)(smem_sm / (smem + fa.sharedSizeBytes + (size_t)reserved));
+    const int by_regs = regs_sm / (regs_warp * (kThreads / 32));
+    n = n < by_smem ? n : by_smem;
+    n = n < by_regs ? n : by_regs;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (dev < 64) cached[dev] = n;
+    *per_sm = n;
+    return cudaSuccess;
+}
+
+cudaError_t beams_plan(int N, int K, int Hq, int Hkv, int max_pages, int num_workers, BeamsPlan* plan) {
+    const size_t R = (size_t)K * (Hq / Hkv);
+    int per_sm = 0, sms = 0;
+    const cudaError_t e = beams_occupancy(&per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    plan->tc_grid = num_workers > 0 ? num_workers : (long long)sms * per_sm;
+    plan->slots = (size_t)plan->tc_grid + (size_t)N * Hkv;  // partial slot = share + segment
+    plan->part_lse_offset = up(plan->slots * R * kHeadDim * 4);
+    plan->merge_list_offset = up(plan->part_lse_offset + plan->slots * R * 4);
+    plan->counts_offset = up(plan->merge_list_offset + (size_t)plan->tc_grid * sizeof(int2));
+    plan->entries_offset = up(plan->counts_offset + (size_t)N * 4);
+    plan->ws_bytes = plan->entries_offset + (size_t)N * K * max_pages * sizeof(PageEntry);
+    return cudaSuccess;
+}
+
+cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, const CUtensorMap& tk,
+                                const CUtensorMap& tv, bool may_split, cudaStream_t stream) {
+    if (args.N == 0) return cudaSuccess;
+    if (args.tc_grid > 0x7fffffffll || args.tc_grid < 1) return cudaErrorInvalidConfiguration;
+    int per_sm = 0, sms = 0;  // also sets the kernel's shared-memory limit
+    cudaError_t e = beams_occupancy(&per_sm, &sms);
+    if (e != cudaSuccess) return e;
+    BeamsArgs a = args;
+    if (!may_split) a.merge_list = nullptr;
+    // one CTA lists a group of up to four steps of columns, a cluster of eight a longer one
+    const int ctas = a.max_pages <= 4 * kPlanThreads ? 1 : 8;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.N * ctas));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    e = a.K <= 4    ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<4>, a)
+        : a.K <= 8  ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<8>, a)
+        : a.K <= 16 ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<16>, a)
+                    : cudaLaunchKernelEx(&cfg, beams_plan_kernel<32>, a);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)a.tc_grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 1024 + sizeof(Smem);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, decode_beams_kernel, tq, tk, tv, a);
+    if (e != cudaSuccess || !may_split) return e;
+    SplitMergeArgs m;
+    m.part_o = a.part_o;
+    m.part_lse = a.part_lse;
+    m.list = a.merge_list;
+    m.out = a.out;
+    m.lse = a.lse;
+    m.listed = (int)a.tc_grid;
+    m.R = a.R;
+    m.G = a.G;
+    m.QL = a.K;
+    m.Hq = a.Hq;
+    m.Hkv = a.Hkv;
+    return split_merge_launch(m, stream);
+}
+
+}  // namespace sinkattn

@@ -9,12 +9,14 @@ if ``libsinkattn.so`` is absent, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 
 import torch
 
-from .abi import (EXPORTS, ERR_BAD_LENGTH, ERR_BAD_PAGE, ERR_CUDA, ERR_INVALID_ARG, ERR_TIMEOUT,  # noqa: F401
-                  ERR_UNSUPPORTED, ERR_WORKSPACE, OK, DecodeDims, MergeDims, PagedDims, PrefillDims, RopeParams,
+from .abi import (DTYPE_BF16, DTYPE_F16, DTYPE_F32, EXPORTS, ERR_BAD_INDEX, ERR_BAD_LENGTH, ERR_BAD_PAGE,  # noqa: F401
+                  ERR_BAD_VALUE, ERR_CUDA, ERR_INVALID_ARG, ERR_NO_PAGES, ERR_TIMEOUT, ERR_UNSUPPORTED, ERR_WORKSPACE,
+                  OK, BeamDims, BeamsDims, DecodeDims, ForkDims, MergeDims, MoveDims, PagedDims, PrefillDims, RopeParams,
                   VerifyDims, declare)
 
 _LIB_PATH = Path(__file__).resolve().parent / "_build" / "libsinkattn.so"
@@ -336,6 +338,231 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
                                       _ptr(sinks), float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims),
                                       _stream(stream))
     _check(st, "sinkattn_decode_noalloc")
+    return out, lse
+
+
+# ---- a beam step over the paged cache -------------------------------------------------------------
+
+_LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _here(*tensors):
+    """The tensors lie on the current device (the one the call's stream belongs to)."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != current:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+
+
+def _on_stream(fn):
+    """Runs a call with its ``stream`` argument current, so that what it allocates (outputs, workspace) belongs to the
+    stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _workspace(workspace, nbytes, device, what):
+    if workspace is not None:
+        return workspace
+    if nbytes == 0:
+        raise SinkAttnError(ERR_INVALID_ARG, what)
+    return torch.empty(nbytes, device=device, dtype=torch.uint8)
+
+
+def _out(t, name, dtype, shape, device):
+    """An output: the given tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, device=device, dtype=dtype)
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    _here(t)
+    return t
+
+
+def beam_dims(logits, num_select, pad_token=0) -> BeamDims:
+    N, K, V = logits.shape
+    stride = logits.stride(1) if K > 1 else (logits.stride(0) if N > 1 else V)
+    return BeamDims(N, K, V, num_select, _LOGIT_DTYPES[logits.dtype], pad_token, stride)
+
+
+def sinkattn_beam_select_workspace_size(logits, num_select) -> int:
+    return int(_lib.sinkattn_beam_select_workspace_size(ctypes.byref(beam_dims(logits, num_select))))
+
+
+@_on_stream
+def sinkattn_beam_select(logits, scores, num_select, finished=None, pad_token=0, out_scores=None, out_parents=None,
+                         out_tokens=None, workspace=None):
+    """The num_select best continuations of each group over its beams and the vocabulary.
+
+    logits [N, K, V] (f32, bf16 or f16; rows may be padded: any stride between them, tokens contiguous), scores
+    [N, K] f32 running log-probabilities, finished [N, K] bool or uint8.  Returns (scores [N, M] f32, parents [N, M]
+    int32 rows n * K + k, tokens [N, M] int32), best first.
+    """
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA tensor")
+    if logits.dtype not in _LOGIT_DTYPES:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    if logits.dim() != 3 or logits.shape[1] == 0 or logits.shape[2] == 0:
+        raise ValueError(f"logits must be [N, K, V], got shape {tuple(logits.shape)}")
+    N, K, V = logits.shape
+    if (V > 1 and logits.stride(2) != 1) or (N > 1 and K > 1 and logits.stride(0) != K * logits.stride(1)):
+        raise ValueError("logits must have contiguous tokens and rows at one distance from each other")
+    _need(scores, "scores", torch.float32, 2)
+    if tuple(scores.shape) != (N, K):
+        raise ValueError("scores must be [N, K]")
+    if finished is not None:
+        _need(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, 2)
+        if tuple(finished.shape) != (N, K):
+            raise ValueError("finished must be [N, K]")
+    _here(logits, scores, finished)
+    M = int(num_select)
+    dims = beam_dims(logits, M, int(pad_token))
+    nbytes = int(_lib.sinkattn_beam_select_workspace_size(ctypes.byref(dims)))
+    if nbytes == 0:
+        st = _lib.sinkattn_beam_select(None, None, None, None, None, None, ctypes.byref(dims), None, 0, None)
+        raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_beam_select")
+    out_scores = _out(out_scores, "out_scores", torch.float32, (N, M), logits.device)
+    out_parents = _out(out_parents, "out_parents", torch.int32, (N, M), logits.device)
+    out_tokens = _out(out_tokens, "out_tokens", torch.int32, (N, M), logits.device)
+    workspace = _workspace(workspace, nbytes, logits.device, "sinkattn_beam_select_workspace_size")
+    st = _lib.sinkattn_beam_select(_ptr(logits), _ptr(scores), _ptr(finished), _ptr(out_scores), _ptr(out_parents),
+                                   _ptr(out_tokens), ctypes.byref(dims), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(), _stream(None))
+    _check(st, "sinkattn_beam_select")
+    return out_scores, out_parents, out_tokens
+
+
+@_on_stream
+def sinkattn_pages_fork(page_table, held_lens, parents, page_refs, keep_lens=None, room_lens=None, grow=0,
+                        out_table=None, out_lens=None, out_refs=None, copies=None, workspace=None):
+    """Page tables and page counts after rows were forked, dropped, trimmed and grown.
+
+    Row r of the new table continues row parents[r] (-1: none) with its first keep_lens[r] tokens (None: all) and has
+    pages for room_lens[r] tokens (None: keep + grow).  ``out_refs`` may be ``page_refs`` itself.  Returns (table [R_out,
+    max_pages], lens [R_out], refs [P], copies [R_out, 3]); ``copies`` goes to sinkattn_kv_copy before the new tokens
+    are written.
+    """
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(held_lens, "held_lens", torch.int32, 1)
+    _need(parents, "parents", torch.int32, 1)
+    _need(page_refs, "page_refs", torch.int32, 1)
+    R, Rin, mp, P = parents.shape[0], page_table.shape[0], page_table.shape[1], page_refs.shape[0]
+    if held_lens.shape[0] != Rin:
+        raise ValueError("held_lens must have one entry per row of page_table")
+    for t, name in ((keep_lens, "keep_lens"), (room_lens, "room_lens")):
+        if t is not None:
+            _need(t, name, torch.int32, 1)
+            if t.shape[0] != R:
+                raise ValueError(f"{name} must have one entry per new row")
+    _here(page_table, held_lens, parents, page_refs, keep_lens, room_lens)
+    dev = page_table.device
+    out_table = _out(out_table, "out_table", torch.int32, (R, mp), dev)
+    out_lens = _out(out_lens, "out_lens", torch.int32, (R,), dev)
+    out_refs = _out(out_refs, "out_refs", torch.int32, (P,), dev)
+    copies = _out(copies, "copies", torch.int32, (R, 3), dev)
+    dims = ForkDims(Rin, R, P, mp, 16, int(grow))
+    if workspace is None:
+        workspace = _workspace(None, int(_lib.sinkattn_pages_fork_workspace_size(ctypes.byref(dims))), dev,
+                               "sinkattn_pages_fork_workspace_size")
+    st = _lib.sinkattn_pages_fork(_ptr(page_table), _ptr(held_lens), _ptr(parents), _ptr(keep_lens), _ptr(room_lens),
+                                  _ptr(page_refs), _ptr(out_table), _ptr(out_lens), _ptr(out_refs), _ptr(copies),
+                                  ctypes.byref(dims), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _stream(None))
+    _check(st, "sinkattn_pages_fork")
+    return out_table, out_lens, out_refs, copies
+
+
+def _pools(k_pages, v_pages):
+    """The pools as [L, P, Hkv, 16, 64]; one layer's pool may come without its first dimension."""
+    _need(k_pages, "k_pages", torch.bfloat16, 5 if k_pages.dim() == 5 else 4)
+    _need(v_pages, "v_pages", torch.bfloat16, k_pages.dim())
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    return k_pages.shape if k_pages.dim() == 5 else (1, *k_pages.shape)
+
+
+@_on_stream
+def sinkattn_kv_copy(k_pages, v_pages, copies):
+    """Copies the first ``tokens`` slots of page src to page dst for every (src, dst, tokens) of copies [n, 3] int32,
+    in place; k_pages / v_pages [P, Hkv, 16, 64] or, for several layers, [L, P, Hkv, 16, 64]."""
+    L, P, Hkv, PS, D = _pools(k_pages, v_pages)
+    _need(copies, "copies", torch.int32, 2)
+    if copies.shape[1] != 3:
+        raise ValueError("copies must be [n, 3]")
+    _here(k_pages, v_pages, copies)
+    dims = MoveDims(L, copies.shape[0], Hkv, D, PS, P, 0, 0)
+    _check(_lib.sinkattn_kv_copy(_ptr(k_pages), _ptr(v_pages), _ptr(copies), ctypes.byref(dims), _stream(None)),
+           "sinkattn_kv_copy")
+
+
+@_on_stream
+def sinkattn_kv_compact(k_pages, v_pages, page_table, start_pos, accepted, num_accepted):
+    """Moves the accepted drafted tokens together, in place: cache position start_pos[b] + accepted[b][i] to
+    start_pos[b] + i for i < num_accepted[b].  Pools as in sinkattn_kv_copy; accepted [B, <= 16] int32."""
+    L, P, Hkv, PS, D = _pools(k_pages, v_pages)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(start_pos, "start_pos", torch.int32, 1)
+    _need(accepted, "accepted", torch.int32, 2)
+    _need(num_accepted, "num_accepted", torch.int32, 1)
+    B = accepted.shape[0]
+    if page_table.shape[0] != B or start_pos.shape[0] != B or num_accepted.shape[0] != B:
+        raise ValueError("inconsistent compact shapes")
+    _here(k_pages, v_pages, page_table, start_pos, accepted, num_accepted)
+    dims = MoveDims(L, B, Hkv, D, PS, P, page_table.shape[1], accepted.shape[1])
+    _check(_lib.sinkattn_kv_compact(_ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(start_pos), _ptr(accepted),
+                                    _ptr(num_accepted), ctypes.byref(dims), _stream(None)), "sinkattn_kv_compact")
+
+
+def beams_dims(q, k_pages, page_table, num_workers=0) -> BeamsDims:
+    N, K, Hq, D = q.shape
+    P, Hkv, PS, _ = k_pages.shape
+    return BeamsDims(N, K, Hq, Hkv, D, PS, P, page_table.shape[2], num_workers)
+
+
+def sinkattn_decode_beams_workspace_size(q, k_pages, page_table, num_workers=0) -> int:
+    return int(_lib.sinkattn_decode_beams_workspace_size(ctypes.byref(beams_dims(q, k_pages, page_table, num_workers))))
+
+
+@_on_stream
+def sinkattn_decode_beams(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=None, lse=None, workspace=None,
+                          num_workers=0, return_lse=True):
+    """Decode of N groups of K rows whose page tables share pages; a shared page is read once per group.
+
+    q [N, K, Hq, 64]; page_table [N, K, max_pages]; kv_lens [N, K].  Returns (out [N, K, Hq, 64], lse [N, K, Hq]).
+    """
+    _need(q, "q", torch.bfloat16, 4)
+    _need(k_pages, "k_pages", torch.bfloat16, 4)
+    _need(v_pages, "v_pages", torch.bfloat16, 4)
+    _need(page_table, "page_table", torch.int32, 3)
+    _need(kv_lens, "kv_lens", torch.int32, 2)
+    _need(sinks, "sinks", torch.float32, 1)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    N, K, Hq, D = q.shape
+    if tuple(page_table.shape[:2]) != (N, K) or tuple(kv_lens.shape) != (N, K) or sinks.shape[0] != Hq:
+        raise ValueError("inconsistent decode_beams shapes")
+    _here(q, k_pages, v_pages, page_table, kv_lens, sinks)
+    dims = beams_dims(q, k_pages, page_table, num_workers)
+    out = _out(out, "out", torch.bfloat16, tuple(q.shape), q.device)
+    if lse is not None or return_lse:
+        lse = _out(lse, "lse", torch.float32, (N, K, Hq), q.device)
+    if workspace is None:
+        nbytes = int(_lib.sinkattn_decode_beams_workspace_size(ctypes.byref(dims)))
+        if nbytes == 0:
+            st = _lib.sinkattn_decode_beams(None, None, None, None, None, None, float(scale), None, None,
+                                            ctypes.byref(dims), None, 0, None)
+            raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_decode_beams")
+        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+    st = _lib.sinkattn_decode_beams(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(sinks),
+                                    float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream(None))
+    _check(st, "sinkattn_decode_beams")
     return out, lse
 
 

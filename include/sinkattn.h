@@ -46,8 +46,18 @@ typedef enum {
     SINKATTN_ERR_BAD_PAGE = 4,     /* device: a page id outside [0, num_pages) was met */
     SINKATTN_ERR_TIMEOUT = 5,      /* device: a pipeline wait gave up; results are invalid */
     SINKATTN_ERR_CUDA = 6,         /* a CUDA runtime call failed */
-    SINKATTN_ERR_BAD_LENGTH = 7    /* device: a kv_len outside [0, max_pages*16] was met */
+    SINKATTN_ERR_BAD_LENGTH = 7,   /* device: a kv_len outside [0, max_pages*16] was met */
+    SINKATTN_ERR_NO_PAGES = 8,     /* device: the pool had fewer free pages than were needed */
+    SINKATTN_ERR_BAD_VALUE = 9,    /* device: a NaN or +infinity where a finite value is needed */
+    SINKATTN_ERR_BAD_INDEX = 10    /* device: a row or token index out of range */
 } sinkattn_status_t;
+
+/* Element types of the tensors that may have more than one. */
+typedef enum {
+    SINKATTN_DTYPE_F32 = 0,
+    SINKATTN_DTYPE_BF16 = 1,
+    SINKATTN_DTYPE_F16 = 2
+} sinkattn_dtype_t;
 
 /* Sizes of a paged decode call. */
 typedef struct {
@@ -388,6 +398,202 @@ sinkattn_status_t sinkattn_decode_noalloc(const void *q, const void *k_pages, co
                                           const int32_t *page_table, const int32_t *kv_lens,
                                           const float *sinks, float scale, void *out, float *lse,
                                           const sinkattn_decode_dims_t *dims, void *stream);
+
+/* ------------------------------------------------------------------------------------------------
+ * A beam step over the paged cache.  N groups (requests) of K rows (beams of a beam search, or samples
+ * of one prompt) each have a page table of their own, and rows share the pages of their common past.
+ * One step of decoding is
+ *   sinkattn_beam_select   the best continuations of each group over its beams and the vocabulary,
+ *   sinkattn_pages_fork    page tables and page counts follow the chosen beams; new pages from the pool,
+ *   sinkattn_kv_copy       copies the last pages that more than one row is about to write (each layer),
+ *   sinkattn_kv_append     the new tokens' keys and values (each layer),
+ *   sinkattn_decode_beams  one query token per row, shared pages read once per group (each layer).
+ * The blog posts describing the method have no counterpart to these calls beyond the per-request KV
+ * pages ("Accelerating Sonar through speculation", section "Inference with speculative decoding").
+ * ------------------------------------------------------------------------------------------------ */
+
+/* Shapes of a beam selection. */
+typedef struct {
+    int32_t num_groups;        /* N groups, 0..65535                                      */
+    int32_t num_beams;         /* K beams per group, 1..32                                */
+    int32_t vocab;             /* V tokens, 1..2^30                                       */
+    int32_t num_select;        /* M continuations chosen per group, 1..64                 */
+    int32_t dtype;             /* sinkattn_dtype_t of the logits                          */
+    int32_t pad_token;         /* the token of a finished beam's continuation, 0..V-1     */
+    int64_t row_stride;        /* elements from one beam's logits to the next's (>= V)    */
+} sinkattn_beam_dims_t;
+
+/* Bytes of device workspace sinkattn_beam_select needs for `dims` on the current device; 0 on invalid dims. */
+size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
+
+/*
+ * Beam search's selection: of the K x V continuations of each group, the M of the highest score
+ *     score(k, v) = scores[n][k] + logits[n][k][v] - ln sum_u exp(logits[n][k][u]),
+ * in descending order; equal scores go to the lower beam, then the lower token.  Scores are compared in
+ * 64 bits (sums of exponentials in 32 bits per thread and 64 across threads).
+ *
+ *   logits    [N, K, V]  f32, bf16 or f16; row (n, k) starts row_stride elements after row (n, k - 1)
+ *   scores    [N, K]     f32   running log-probability of each beam; -inf: the beam is not in use, its
+ *                              logits are not read and it has no continuation
+ *   finished  [N, K]     uint8 or NULL: a beam with a non-zero flag has one continuation, pad_token at its
+ *                              unchanged score; its logits are not read
+ *   out_scores  [N, M]   f32
+ *   out_parents [N, M]   int32 row n * K + k of the beam continued (as sinkattn_pages_fork takes it)
+ *   out_tokens  [N, M]   int32
+ *   workspace  at least sinkattn_beam_select_workspace_size(dims) bytes, 256-byte aligned; it needs no
+ *              initialisation and must not be shared by calls that may overlap.
+ *
+ * A logit of -inf is no continuation.  Where a group has fewer than M, the rest of its row is score -inf,
+ * parent -1, token -1.  A beam in use whose score is NaN or +inf, or whose logits hold a NaN or +inf, has
+ * no continuation and raises SINKATTN_ERR_BAD_VALUE.
+ */
+sinkattn_status_t sinkattn_beam_select(const void *logits, const float *scores, const uint8_t *finished,
+                                       float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                                       const sinkattn_beam_dims_t *dims, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/* Shapes of a fork of page tables. */
+typedef struct {
+    int32_t num_rows_in;       /* rows of the present page table, 0..2^20                 */
+    int32_t num_rows_out;      /* rows of the new page table, 0..2^20                     */
+    int32_t num_pages;         /* P, pages of the pool                                    */
+    int32_t max_pages;         /* row length of both page tables (>= 1)                   */
+    int32_t page_size;         /* must be 16                                              */
+    int32_t grow;              /* room for new tokens per row where room_lens is NULL (>= 0) */
+} sinkattn_fork_dims_t;
+
+/* Bytes of device workspace sinkattn_pages_fork needs for `dims`; 0 on invalid dims. */
+size_t sinkattn_pages_fork_workspace_size(const sinkattn_fork_dims_t *dims);
+
+/*
+ * Page tables after a step: forks, drops, trims and grows rows, and counts the holders of every page.
+ * A page of the pool is free while its count is 0.  Row r of the new table continues row p = parents[r] of
+ * the present one with its first keep_lens[r] tokens and has room for room_lens[r]; every row of the
+ * present table ends.  So a parent named by several rows is forked, one named by none is freed, and
+ * parents[r] = -1 starts an empty row (a new request: keep 0, room = its prompt).
+ *   - Pages of kept tokens are shared: the new row holds the parent's pages.
+ *   - A row that keeps part of its last page and has room for more is going to write that page.  It stays
+ *     in it only if the parent's row is its one holder (count 1), every row that continues this parent
+ *     keeps the same number of tokens and has room for more, and r is the first of them.  Otherwise it
+ *     gets a new page in its place, and copies[r] tells sinkattn_kv_copy what to bring there.
+ *   - New pages are the lowest-numbered pages that are free when the call begins, dealt to the rows in
+ *     order (first the replaced page, then the following columns).
+ * Every result is a whole number and the same however the call is scheduled.
+ *
+ *   page_table  [R_in, max_pages]   int32   present table; columns past a row's held tokens are not read
+ *   held_lens   [R_in]              int32   tokens that each present row has pages for
+ *   parents     [R_out]             int32   -1 or a row of the present table
+ *   keep_lens   [R_out]             int32   tokens kept of the parent (0..held), or NULL: all of them
+ *   room_lens   [R_out]             int32   tokens the new row needs pages for (keep..max_pages*16), or
+ *                                           NULL: keep + dims->grow (0 for a row without parent)
+ *   page_refs   [P]                 int32   holders of each page
+ *   out_table   [R_out, max_pages]  int32   the new table, -1 in unused columns
+ *   out_lens    [R_out]             int32   room of each new row (held_lens of the next call)
+ *   out_refs    [P]                 int32   the new counts; may be page_refs itself
+ *   copies      [R_out, 3]          int32   (source page, destination page, tokens), or (-1, -1, 0)
+ *   workspace   at least sinkattn_pages_fork_workspace_size(dims) bytes, 256-byte aligned; it needs no
+ *               initialisation and must not be shared by calls that may overlap.
+ * out_table, out_lens and copies must not overlap the inputs.  Either table may have no rows.
+ *
+ * With fewer free pages than needed nothing is done: counts stay, out_table is -1, out_lens 0, copies empty
+ * and SINKATTN_ERR_NO_PAGES is raised (the present table stays valid).  A parent outside [-1, R_in) counts
+ * as -1 (SINKATTN_ERR_BAD_INDEX); lengths outside their range are clamped (SINKATTN_ERR_BAD_LENGTH); a
+ * held page id outside [0, P) is carried along uncounted (SINKATTN_ERR_BAD_PAGE).
+ */
+sinkattn_status_t sinkattn_pages_fork(const int32_t *page_table, const int32_t *held_lens,
+                                      const int32_t *parents, const int32_t *keep_lens,
+                                      const int32_t *room_lens, const int32_t *page_refs,
+                                      int32_t *out_table, int32_t *out_lens, int32_t *out_refs,
+                                      int32_t *copies, const sinkattn_fork_dims_t *dims, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/* Shapes of the calls that move cached tokens inside the pools of one or several layers. */
+typedef struct {
+    int32_t num_layers;        /* L pools one behind the other: [L, P, Hkv, 16, 64] (>= 1) */
+    int32_t num_rows;          /* copies (kv_copy) or requests (kv_compact), 0..2^20      */
+    int32_t num_kv_heads;      /* Hkv                                                     */
+    int32_t head_dim;          /* must be 64                                              */
+    int32_t page_size;         /* must be 16                                              */
+    int32_t num_pages;         /* P, pages of one layer's pool                            */
+    int32_t max_pages;         /* kv_compact: row length of page_table (>= 1)             */
+    int32_t max_accepted;      /* kv_compact: row length of accepted, 1..16               */
+} sinkattn_move_dims_t;
+
+/*
+ * Copies pages: the first `tokens` slots of every KV head of page src to page dst, keys and values, in
+ * every layer.  Slots of dst past them keep what they held.
+ *
+ *   k_pages, v_pages  [L, P, Hkv, 16, 64]  bf16, in place
+ *   copies            [num_rows, 3] int32  (src, dst, tokens), tokens 0..16; (-1, -1, any) is skipped
+ *
+ * No destination may be another entry's source or destination (sinkattn_pages_fork's copies are such);
+ * entries that break this leave one or the other in the page.  A page id outside [0, P) skips the entry
+ * (SINKATTN_ERR_BAD_PAGE), tokens outside [0, 16] are clamped (SINKATTN_ERR_BAD_LENGTH).
+ */
+sinkattn_status_t sinkattn_kv_copy(void *k_pages, void *v_pages, const int32_t *copies,
+                                   const sinkattn_move_dims_t *dims, void *stream);
+
+/*
+ * After the verification of drafted tokens: moves the accepted ones together.  The keys and values at
+ * cache position start_pos[b] + accepted[b][i] go to start_pos[b] + i for i < num_accepted[b], in every
+ * KV head and layer, as if all were read before any is written.
+ *
+ *   k_pages, v_pages  [L, P, Hkv, 16, 64]  bf16, in place
+ *   page_table    [B, max_pages]     int32 (B = num_rows)
+ *   start_pos     [B]                int32 cache position of drafted token 0
+ *   accepted      [B, max_accepted]  int32 drafted tokens kept, in their new order (entries past
+ *                                          num_accepted are not read)
+ *   num_accepted  [B]                int32 0..max_accepted
+ *
+ * The pages written must be held by one request only.  A position outside [0, max_pages * 16) skips its token
+ * and raises SINKATTN_ERR_BAD_LENGTH, as does a num_accepted out of range (clamped); a page id outside
+ * [0, P) skips its token and raises SINKATTN_ERR_BAD_PAGE; an accepted index below 0 skips its token and
+ * raises SINKATTN_ERR_BAD_INDEX.
+ */
+sinkattn_status_t sinkattn_kv_compact(void *k_pages, void *v_pages, const int32_t *page_table,
+                                      const int32_t *start_pos, const int32_t *accepted,
+                                      const int32_t *num_accepted, const sinkattn_move_dims_t *dims,
+                                      void *stream);
+
+/* Shapes of a decode of groups of rows that share pages. */
+typedef struct {
+    int32_t num_groups;        /* N groups, 0..32768                                      */
+    int32_t num_beams;         /* K rows per group, 1..32, and K * Hq / Hkv <= 128        */
+    int32_t num_q_heads;       /* Hq                                                      */
+    int32_t num_kv_heads;      /* Hkv, divides Hq                                         */
+    int32_t head_dim;          /* must be 64                                              */
+    int32_t page_size;         /* must be 16                                              */
+    int32_t num_pages;         /* P, pages in the K/V pools                               */
+    int32_t max_pages;         /* row length of page_table (>= 1)                         */
+    int32_t num_workers;       /* as in sinkattn_decode_dims_t (0 = automatic)            */
+} sinkattn_beams_dims_t;
+
+/* Bytes of device workspace sinkattn_decode_beams needs for `dims` on the current device; 0 on invalid dims. */
+size_t sinkattn_decode_beams_workspace_size(const sinkattn_beams_dims_t *dims);
+
+/*
+ * sinkattn_decode for groups of rows that share pages: every row attends to its own cached tokens, and a
+ * page that several rows of a group hold in the same column is read once for all of them.  The result is
+ * that of sinkattn_decode on the N * K rows.
+ *
+ *   q          [N, K, Hq, 64]          bf16   one query token per row
+ *   k_pages, v_pages [P, Hkv, 16, 64]  bf16
+ *   page_table [N, K, max_pages]       int32  entries past a row's last page are never read
+ *   kv_lens    [N, K]                  int32  cached tokens per row, 0..max_pages*16 (rows of a group may
+ *                                             differ)
+ *   sinks      [Hq]                    f32
+ *   out        [N, K, Hq, 64]          bf16
+ *   lse        [N, K, Hq]              f32 natural log, or NULL
+ *   workspace  at least sinkattn_decode_beams_workspace_size(dims) bytes, 256-byte aligned; it needs no
+ *              initialisation and must not be shared by calls that may overlap.
+ *
+ * Errors and the handling of bad page ids and lengths are those of sinkattn_decode.
+ */
+sinkattn_status_t sinkattn_decode_beams(const void *q, const void *k_pages, const void *v_pages,
+                                        const int32_t *page_table, const int32_t *kv_lens,
+                                        const float *sinks, float scale, void *out, float *lse,
+                                        const sinkattn_beams_dims_t *dims, void *workspace,
+                                        size_t workspace_bytes, void *stream);
 
 /*
  * Takes and clears the current device's error word in one atomic step ordered

@@ -1,0 +1,268 @@
+"""Beam search's selection on the GPU against numpy in 64 bits, through the C ABI.
+
+Tolerance.  A thread adds at most 65536 / 16 / 256 groups of 16 exponentials into four 32-bit sums, 64 additions
+each: 64 x 2^-24 relative in the worst case; an exponential is off by 2^-22 (the instruction's bound) plus 2^-24 times
+its argument, whose terms weigh e^argument (x e^-x <= 0.37); the groups' order adds nothing.  Together the log-sum-exp is
+off by at most 5e-6, and a returned 32-bit score by that plus half a step of its own.  Picks have to be the reference's
+wherever its next score is further away than twice that.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+LSE_TOL = 5e-6
+
+
+@pytest.fixture(scope="module")
+def S():
+    from gqa_attention_learned_head_gb300 import sinkattn
+
+    return sinkattn
+
+
+def reference(logits, scores, M, finished=None, pad=0):
+    """(scores, parents, tokens) [N, M], and every group's sorted scores."""
+    z = logits.double().cpu().numpy()
+    c = scores.double().cpu().numpy()
+    N, K, V = z.shape
+    out_s, out_p, out_t = np.full((N, M), -np.inf), np.full((N, M), -1), np.full((N, M), -1)
+    for n in range(N):
+        rows = np.full((K, V), -np.inf)
+        for k in range(K):
+            if not np.isfinite(c[n, k]):
+                continue
+            if finished is not None and bool(finished[n, k]):
+                rows[k, pad] = c[n, k]
+                continue
+            m = z[n, k].max()
+            if not np.isfinite(m) or np.isnan(z[n, k]).any():
+                continue
+            lse = m + np.log(np.exp(z[n, k] - m).sum())
+            rows[k] = c[n, k] + (z[n, k] - lse)
+        flat = rows.reshape(-1)
+        top = np.lexsort((np.arange(flat.size), -flat))[:M]
+        top = top[flat[top] > -np.inf]
+        out_s[n, :top.size] = flat[top]
+        out_p[n, :top.size] = n * K + top // V
+        out_t[n, :top.size] = top % V
+    return out_s, out_p, out_t
+
+
+def check(got, ref, exact=False):
+    gs, gp, gt = (t.cpu().numpy() for t in got)
+    rs, rp, rt = ref
+    assert np.array_equal(np.isneginf(gs), np.isneginf(rs))
+    live = ~np.isneginf(rs)
+    err = np.abs(gs[live] - rs[live])
+    assert np.all(err <= LSE_TOL + 2.0 ** -24 * np.abs(rs[live])), err.max()
+    with np.errstate(invalid="ignore"):
+        gap = np.minimum(np.abs(np.diff(rs, axis=1, prepend=np.inf)), np.abs(np.diff(rs, axis=1, append=-np.inf)))
+    # (the last pick's rival is not in the list: its score was compared above)
+    sure = np.ones_like(live) if exact else ~live | (np.nan_to_num(gap, nan=np.inf) > 2 * LSE_TOL)
+    sure[:, -1] &= exact | ~live[:, -1]
+    assert np.array_equal(gp[sure], rp[sure]) and np.array_equal(gt[sure], rt[sure])
+
+
+def make(N, K, V, dtype, seed, std=2.5):
+    g = torch.Generator().manual_seed(seed)
+    z = (torch.randn(N, K, V, generator=g) * std).to(dtype).cuda()
+    c = (-20 * torch.rand(N, K, generator=g)).cuda()
+    return z, c
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("N,K,V,M", [(1, 1, 1, 1), (1, 1, 5, 3), (2, 3, 15, 8), (1, 4, 16, 64), (3, 2, 17, 5),
+                                     (1, 32, 257, 64), (2, 8, 4099, 16), (1, 4, 32000, 8), (5, 3, 50021, 6),
+                                     (1, 2, 200003, 4), (2, 1, 131072, 64)])
+def test_sizes(S, dtype, N, K, V, M):
+    z, c = make(N, K, V, dtype, seed=N + K + V + M)
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    check(got, reference(z, c, M))
+
+
+def test_more_rows_than_resident_shares(S):
+    z, c = make(400, 4, 1003, torch.bfloat16, seed=5)
+    got = S.sinkattn_beam_select(z, c, 8)
+    assert S.sinkattn_get_error() == 0
+    check(got, reference(z, c, 8))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("pad,first", [(1, 0), (3, 1), (24, 8), (0, 5)])
+def test_padded_rows_and_odd_starts(S, dtype, pad, first):
+    """Rows at any distance, starting at any element of the buffer: the same picks, and the padding is not read as
+    logits (it holds the largest values)."""
+    N, K, V, M = 2, 3, 5003, 7
+    z, c = make(N, K, V, dtype, seed=9)
+    buf = torch.full((first + N * K * (V + pad),), 1e4, dtype=dtype, device="cuda")
+    view = torch.as_strided(buf, (N, K, V), (K * (V + pad), V + pad, 1), first)
+    view.copy_(z)
+    a, b = S.sinkattn_beam_select(z, c, M), S.sinkattn_beam_select(view, c, M)
+    assert S.sinkattn_get_error() == 0
+    check(b, reference(z, c, M))
+    for x, y in zip(a, b):  # sums run in the tokens' order wherever a row starts: the same bits
+        assert torch.equal(x, y)
+
+
+def test_equal_beams_and_equal_logits_go_to_the_lowest(S):
+    """Ties of every kind: identical beams (as at a search's first step), constant rows, long runs of one value."""
+    N, K, V, M = 2, 4, 10007, 12
+    z, c = make(N, 1, V, torch.float32, seed=3)
+    z, c = z.expand(N, K, V).contiguous(), c[:, :1].expand(N, K).contiguous()
+    check(S.sinkattn_beam_select(z, c, M), reference(z, c, M), exact=True)
+    z = torch.full((N, K, V), -1.5, device="cuda", dtype=torch.bfloat16)
+    s, p, t = S.sinkattn_beam_select(z, c, M)
+    assert torch.equal(t.cpu(), torch.arange(M, dtype=torch.int32).expand(N, M))
+    assert torch.equal(p.cpu(), (torch.arange(N, dtype=torch.int32) * K)[:, None].expand(N, M))
+    z[:, 2, 7000:] = 4.0
+    check(S.sinkattn_beam_select(z, c, 64), reference(z, c, 64), exact=True)
+
+
+@pytest.mark.parametrize("order", [1, -1])
+def test_sorted_logits(S, order):
+    """Rising or falling logits: the best all lie in one thread's, or neighbouring, groups."""
+    V = 70000
+    z = (torch.arange(V, dtype=torch.float32) * order / 1000).expand(1, 2, V).contiguous().cuda()
+    c = torch.tensor([[-1.0, -1.25]]).cuda()
+    check(S.sinkattn_beam_select(z, c, 33), reference(z, c, 33))
+
+
+def test_best_tokens_in_one_threads_groups(S):
+    """The best tokens at a distance of 256 groups: one thread meets them all."""
+    V = 65536
+    z, c = make(1, 1, V, torch.float32, seed=8)
+    z[0, 0, ::4096] += 40
+    z[0, 0, 5::4096] += 41
+    check(S.sinkattn_beam_select(z, c, 40), reference(z, c, 40))
+
+
+def test_finished_and_unused_beams(S):
+    N, K, V, M = 3, 5, 3001, 10
+    z, c = make(N, K, V, torch.bfloat16, seed=4)
+    c[0, 1:] = -math.inf  # the first step: one beam in use
+    c[2, :] = -math.inf
+    done = torch.zeros(N, K, dtype=torch.bool, device="cuda")
+    done[1, 0] = done[1, 3] = done[0, 4] = True
+    z[0, 1:] = float("nan")  # logits that are not to be read
+    z[1, 3] = float("nan")
+    got = S.sinkattn_beam_select(z, c, M, finished=done, pad_token=17)
+    assert S.sinkattn_get_error() == 0
+    check(got, reference(z, c, M, done, 17))
+    everyone = torch.ones(N, K, dtype=torch.uint8, device="cuda")
+    s, p, t = S.sinkattn_beam_select(z, c, M, finished=everyone, pad_token=3000)
+    assert S.sinkattn_get_error() == 0
+    check((s, p, t), reference(z, c, M, everyone, 3000), exact=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_masked_tokens(S, dtype):
+    """-inf tokens are no continuations; masks of the type's lowest value are very unlikely ones."""
+    N, K, V, M = 2, 3, 9001, 20
+    z, c = make(N, K, V, dtype, seed=6)
+    z[0, 0, :] = -math.inf           # a row without a token
+    z[0, 1, 5:] = -math.inf          # five tokens left
+    z[0, 2, 100:8990] = -math.inf
+    lowest = torch.finfo(dtype).min
+    z[1, 0, 7:] = lowest
+    z[1, 1, :] = lowest              # uniform, at the bottom of the type's range
+    z[1, 2, :] = -math.inf
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    rs, rp, rt = reference(z, c, M)
+    gs, gp, gt = (t.cpu().numpy() for t in got)
+    assert np.allclose(gs, rs, rtol=2.0 ** -22, atol=LSE_TOL)
+    assert np.array_equal(gp, rp) and np.array_equal(gt, rt)
+
+
+@pytest.mark.parametrize("value", [3e5, 2e6, 1e30, -2e6, -3e38])
+def test_large_logits(S, value):
+    """Rows around a value whose product with log2 e has no fraction left, or overflows."""
+    V, M = 5000, 6
+    z = torch.full((1, 2, V), value, device="cuda")
+    z[0, 0, 3000] = value + abs(value) * 1e-5
+    z[0, 1, 17] = -math.inf
+    c = torch.tensor([[-2.0, -1.0]]).cuda()
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    rs, rp, rt = reference(z, c, M)
+    gs, gp, gt = (t.cpu().numpy() for t in got)
+    assert np.allclose(gs, rs, rtol=2.0 ** -22, atol=LSE_TOL)
+    assert np.array_equal(gp, rp) and np.array_equal(gt, rt)
+
+
+@pytest.mark.parametrize("where", ["nan", "inf", "nan score", "inf score", "nan among masked"])
+def test_bad_values_are_reported_and_their_beam_left_out(S, where):
+    N, K, V, M = 2, 3, 20011, 5
+    z, c = make(N, K, V, torch.float32, seed=7)
+    if where == "nan":
+        z[1, 1, 19999] = float("nan")
+    elif where == "inf":
+        z[1, 1, 3] = math.inf
+    elif where == "nan among masked":
+        z[1, 1, :] = -math.inf
+        z[1, 1, 12345] = float("nan")
+    else:
+        c[1, 1] = float("nan") if where == "nan score" else math.inf
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == S.ERR_BAD_VALUE
+    c2 = c.clone()
+    c2[1, 1] = -math.inf
+    check(got, reference(torch.nan_to_num(z, posinf=0.0), c2, M))
+    assert S.sinkattn_get_error() == 0
+
+
+def test_groups_and_empty_call(S):
+    z, c = make(1, 2, 100, torch.float32, seed=1)
+    s, p, t = S.sinkattn_beam_select(z[:0], c[:0], 4)
+    assert s.shape == (0, 4) and p.shape == (0, 4) and t.shape == (0, 4)
+
+
+def test_replayed_from_a_graph_and_on_another_stream(S):
+    z, c = make(3, 4, 8009, torch.bfloat16, seed=11)
+    out = [torch.empty(3, 8, dtype=d, device="cuda") for d in (torch.float32, torch.int32, torch.int32)]
+    ws = torch.empty(S.sinkattn_beam_select_workspace_size(z, 8), dtype=torch.uint8, device="cuda")
+    call = lambda **kw: S.sinkattn_beam_select(z, c, 8, out_scores=out[0], out_parents=out[1],  # noqa: E731
+                                               out_tokens=out[2], workspace=ws, **kw)
+    call()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    z2, c2 = make(3, 4, 8009, torch.bfloat16, seed=12)
+    z.copy_(z2)
+    c.copy_(c2)
+    g.replay()
+    torch.cuda.synchronize()
+    check(out, reference(z2, c2, 8))
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    got = S.sinkattn_beam_select(z, c, 8, stream=other)
+    other.synchronize()
+    for x, y in zip(got, out):
+        assert torch.equal(x, y)
+
+
+def test_refusals(S):
+    z, c = make(2, 3, 100, torch.float32, seed=2)
+    with pytest.raises(TypeError):
+        S.sinkattn_beam_select(z.double(), c, 4)
+    with pytest.raises(TypeError):
+        S.sinkattn_beam_select(z.cpu(), c, 4)
+    with pytest.raises(TypeError):
+        S.sinkattn_beam_select(z, c.half(), 4)
+    with pytest.raises(ValueError):
+        S.sinkattn_beam_select(z, c[:1], 4)
+    with pytest.raises(ValueError):
+        S.sinkattn_beam_select(z.transpose(1, 2), c, 4)
+    with pytest.raises(ValueError):
+        S.sinkattn_beam_select(z, c, 4, finished=torch.zeros(2, 2, dtype=torch.bool, device="cuda"))
+    for M, pad in ((0, 0), (65, 0), (4, 100), (4, -1)):
+        with pytest.raises(S.SinkAttnError):
+            S.sinkattn_beam_select(z, c, M, pad_token=pad)
+    with pytest.raises(S.SinkAttnError) as e:
+        S.sinkattn_beam_select(z, c, 4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == S.ERR_WORKSPACE
