@@ -8,7 +8,7 @@ namespace sinkattn {
 constexpr int kDtF32 = 0, kDtBf16 = 1, kDtF16 = 2;  // sinkattn_dtype_t
 constexpr int kBeamMaxBeams = 32;    // K
 constexpr int kBeamMaxSelect = 64;   // M
-constexpr int kBeamMaxPart = 65536;  // tokens of one row that one CTA reads at most
+constexpr int kBeamMaxPart = 262144;  // tokens of one row that one CTA reads at most
 
 constexpr int kBeamMaxCands = 8192;  // K x shares of a row x M: candidates that meet in the merge
 

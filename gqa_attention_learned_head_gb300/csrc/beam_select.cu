@@ -10,16 +10,16 @@
 //   above that is in 64 bits: the scores of two beams may lie next to each other.  lse = (r + log2 s) / L
 //   with the same rounded L, so its rounding cancels to first order.  Where the largest logit is beyond
 //   +-2^20 (rows of nothing but a type's lowest value) the share is read again and summed as e^(x - m).
-//   Best tokens.  The row is cut into groups of 16 tokens whose maxima stay in shared memory.  The M best
-//   tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there
-//   are M tokens ahead.  So the pass over the row has no list to maintain; afterwards the M best of the
-//   threads' maxima give a threshold, the groups at or above it (M or a few more) are ranked by counting,
-//   and the 16 M tokens of the M best are read again and ranked the same way.  Keys are (order of the value,
-//   ~position), all different, so ties need no case of their own.
+//   Best tokens.  The row is cut into groups of 32 consecutive tokens whose maxima stay in shared memory.  The M
+//   best tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there
+//   are M tokens ahead.  So the pass over the row has no list to maintain; afterwards the M-th best of the
+//   64 maxima that quads of threads have met is a threshold, the groups at or above it (M or a few more) are
+//   ranked by counting, and the 32 M tokens of the M best are read again and ranked the same way.  Keys are
+//   (order of the value, ~position), all different, so ties need no case of their own.
 //
-// Two kernels: select_rows_kernel, one CTA per share of a row (a row is cut into as many shares as fill the
-// GPU), bound by HBM (one read of the logits) with the exponentials close behind (one MUFU operation per
-// logit); select_merge_kernel, one CTA per group, launched as its programmatic dependent.
+// Two kernels: select_rows_kernel, one CTA per share of a row (rows are cut into as many shares as run at once),
+// bound by HBM (one read of the logits) with the exponentials close behind (one MUFU operation per logit);
+// select_merge_kernel, one CTA per group, launched as its programmatic dependent.
 #include "args_beam.h"
 #include "ptx.cuh"
 
@@ -29,10 +29,10 @@ namespace sinkattn {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 16;  // tokens of a group: 32 or 64 bytes, a thread's loads of one step
-constexpr int kMaxGroups = kBeamMaxPart / kGroup;
-constexpr int kListCap = kBeamMaxSelect * kMaxGroups / kThreads;  // at most M threads' groups pass the threshold
-static_assert(kListCap >= kBeamMaxSelect * kGroup, "the token list uses the group list's room");
+constexpr int kUnit = 16;             // consecutive tokens that a thread takes at a time: 32 or 64 bytes
+constexpr int kGroup = 2 * kUnit;     // tokens of a group, held by two neighbouring threads
+constexpr int kQuads = kThreads / 4;  // quads of threads; each quad's best group enters the threshold
+static_assert(kQuads >= kBeamMaxSelect, "the threshold needs M maxima");
 constexpr float kL = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kInf = __builtin_huge_valf();
@@ -91,39 +91,53 @@ struct Elem<kDtF16> {
     }
 };
 
-// A row's share: where it starts, and which of its groups can be read in 16-byte pieces.
+// 32 bytes from a 32-byte boundary: one whole sector a thread.
+__device__ __forceinline__ void load32(const void* p, uint32_t* r) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
+
+// A row's share: where it starts, and which of its units can be read in whole pieces.
 template <int DT>
 struct Share {
     using E = Elem<DT>;
     using T = typename E::T;
-    static constexpr int kWords = kGroup * (int)sizeof(T) / 4;  // 32-bit words of a group
-    const T* p;       // first token of the share
-    int len, groups;  // tokens, groups (the last may be partial)
-    int off;          // bytes from the 16-byte boundary at or below p (0..15), the same for every group
-    int lo, hi;       // groups [lo, hi) are whole and their 16-byte pieces lie inside the tensor
+    static constexpr int kWords = kUnit * (int)sizeof(T) / 4;  // 32-bit words of a unit
+    const T* p;      // first token of the share
+    int len, units;  // tokens, units (the last may be partial)
+    int off;         // bytes from the 16-byte boundary at or below p (0..15), the same for every unit
+    bool sectors;    // units start at 32-byte boundaries
+    int lo, hi;      // units [lo, hi) are whole and their 16-byte pieces lie inside the tensor
 
     __device__ void set(const T* tensor, const T* tensor_end, const T* first, int n) {
         p = first;
         len = n;
-        groups = (n + kGroup - 1) / kGroup;
+        units = (n + kUnit - 1) / kUnit;
         off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-        hi = n / kGroup;
+        sectors = (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+        hi = n / kUnit;
         lo = 0;
-        if (off) {  // a group's pieces then start before it and end behind it
+        if (off) {  // a unit's pieces then start before it and end behind it
             const char* c = reinterpret_cast<const char*>(p) - off;
             if (c < reinterpret_cast<const char*>(tensor)) lo = 1;
             if (hi > 0 && c + hi * (kWords * 4) + 16 > reinterpret_cast<const char*>(tensor_end)) --hi;
         }
     }
-    // Group g's values as words: 16-byte pieces, shifted together if the row is not aligned to them; token by
-    // token at the tensor's edges and past the share's end (-inf there).
-    __device__ void load(int g, uint32_t (&w)[kWords]) const {
-        if (g >= lo && g < hi) {
-            const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(p) - off + (size_t)g * (kWords * 4));
-            if (off == 0) {
+    // Unit u's values as words: whole sectors, or 16-byte pieces, shifted together if the row is not aligned to
+    // them; token by token at the tensor's edges and past the share's end (-inf there).  The thread that holds a
+    // token, and so the order of every sum, does not depend on where the row starts.
+    __device__ void load(int u, uint32_t (&w)[kWords]) const {
+        if (u >= lo && u < hi) {
+            const char* c = reinterpret_cast<const char*>(p) - off + (size_t)u * (kWords * 4);
+            const uint4* v = reinterpret_cast<const uint4*>(c);
+            if (sectors) {
+#pragma unroll
+                for (int i = 0; i < kWords / 8; ++i) load32(c + 32 * i, &w[8 * i]);
+            } else if (off == 0) {
 #pragma unroll
                 for (int i = 0; i < kWords / 4; ++i) {
-                    const uint4 q = __ldcg(v + i);
+                    const uint4 q = v[i];
                     w[4 * i] = q.x;
                     w[4 * i + 1] = q.y;
                     w[4 * i + 2] = q.z;
@@ -147,21 +161,26 @@ struct Share {
 #pragma unroll
                     for (int i = 0; i < kWords + 1; ++i) r[i] = r[i + 1];
                 }
-                const int bits = 8 * (off & 3);
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], bits);
+                    for (int i = 0; i < kWords; ++i) w[i] = r[i];
+                } else {
+                    const int bits = 8 * (off & 3);
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], bits);
+                }
             }
         } else {
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 if constexpr (sizeof(T) == 4) {
-                    const int e = g * kGroup + i;
+                    const int e = u * kUnit + i;
                     w[i] = e < len ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(p) + e)) : E::kNone;
                 } else {
-                    const int e = g * kGroup + 2 * i;
-                    const unsigned a = e < len ? (unsigned)__ldcg(reinterpret_cast<const unsigned short*>(p) + e) : E::kNone;
-                    const unsigned b =
-                        e + 1 < len ? (unsigned)__ldcg(reinterpret_cast<const unsigned short*>(p) + e + 1) : E::kNone;
+                    const int e = u * kUnit + 2 * i;
+                    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+                    const unsigned a = e < len ? (unsigned)__ldcg(h + e) : E::kNone;
+                    const unsigned b = e + 1 < len ? (unsigned)__ldcg(h + e + 1) : E::kNone;
                     w[i] = a | (b << 16);
                 }
             }
@@ -184,7 +203,7 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ int rank_of(const unsigned long long* keys, int n, unsigned long long key) {
     int r = 0;
     const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(keys);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < n / 2; ++i) {
         const ulonglong2 k = k2[i];
         r += (k.x > key) + (k.y > key);
@@ -193,26 +212,33 @@ __device__ __forceinline__ int rank_of(const unsigned long long* keys, int n, un
 }
 
 struct SelectSmem {
-    alignas(16) unsigned long long top[kThreads];  // the threads' best groups
-    alignas(16) unsigned long long list[kListCap + 2];
-    float gmax[kMaxGroups];
+    alignas(16) unsigned long long top[kQuads];  // the quads' best groups
+    float s[kThreads], r[kThreads];              // the threads' sums and references
     int sel[kBeamMaxSelect];
     unsigned long long threshold;
-    float red_m[kThreads / 32], red_r[kThreads / 32];
-    double red_s[kThreads / 32];
-    int count;
+    int found[2];  // entries of the two lists
 };
+// Behind it: the groups at or above the threshold (M quads' at most), the tokens of the M best, every group's maximum.
+__host__ __device__ inline int groups_of(int tokens) { return (tokens + kGroup - 1) / kGroup; }
+__host__ __device__ inline int list_cap(int groups, int M) {  // a quad has two of every 2 kQuads groups
+    return M * 2 * ((groups + 2 * kQuads - 1) / (2 * kQuads));
+}
+__host__ __device__ inline size_t select_smem(int part_len, int M) {
+    const int groups = groups_of(part_len);
+    return sizeof(SelectSmem) + ((size_t)list_cap(groups, M) + M * kGroup + 2) * 8 + (size_t)groups * 4;
+}
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads) select_rows_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs a) {
     using E = Elem<DT>;
     using T = typename E::T;
     constexpr int kWords = Share<DT>::kWords;
-    constexpr int kBatch = 32 / kWords;  // groups loaded together: 128 bytes a thread
-    __shared__ SelectSmem sm;
+    constexpr int kBatch = 32 / kWords;  // units loaded together: 128 bytes a thread
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, M = a.M;
     const int row = (int)(blockIdx.x / (unsigned)a.parts), part = (int)(blockIdx.x % (unsigned)a.parts);
     // a finished beam, or one that is not in use, is not read (the merge does not look at its shares)
     if (a.finished && __ldcg(&a.finished[row])) return;
@@ -226,36 +252,41 @@ __global__ void __launch_bounds__(kThreads) select_rows_kernel(const BeamArgs a)
         const T* end = base + ((long long)a.N * a.K - 1) * a.row_stride + a.V;
         sh.set(base, end, base + row * a.row_stride + e0, min(a.part_len, a.V - e0));
     }
+    const int groups = groups_of(sh.len);
+    unsigned long long* list = reinterpret_cast<unsigned long long*>(&sm + 1);
+    unsigned long long* tokens = list + list_cap(groups_of(a.part_len), M);
+    float* gmax = reinterpret_cast<float*>(tokens + M * kGroup + 2);
 
-    // ---- 1. one pass over the share: sums, and every group's maximum
+    // ---- 1. one pass over the share: sums, and every group's maximum.  A group is two neighbouring threads' units.
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     float r2 = -1e9f, best = kNegInf;
     int best_g = 0;
-    for (int g0 = tid; g0 < sh.groups; g0 += kThreads * kBatch) {
+    for (int u0 = tid; u0 - lane < sh.units; u0 += kThreads * kBatch) {  // whole warps
         uint32_t w[kBatch][kWords];
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int g = g0 + u * kThreads;
-            if (g < sh.groups) {
-                sh.load(g, w[u]);
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = u0 + b * kThreads;
+            if (u < sh.units) {
+                sh.load(u, w[b]);
             } else {
 #pragma unroll
-                for (int i = 0; i < kWords; ++i) w[u][i] = sizeof(T) == 4 ? E::kNone : E::kNone * 0x10001u;
+                for (int i = 0; i < kWords; ++i) w[b][i] = sizeof(T) == 4 ? E::kNone : E::kNone * 0x10001u;
             }
         }
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int g = g0 + u * kThreads;
-            float x[kGroup];
-            E::unpack(w[u], x);
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = u0 + b * kThreads;
+            float x[kUnit];
+            E::unpack(w[b], x);
             float m4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
-            const float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-            if (g < sh.groups) sm.gmax[g] = gm;
+            float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
+            if (!(tid & 1) && u < sh.units) gmax[u >> 1] = gm;
             if (gm > best) {
                 best = gm;
-                best_g = g;
+                best_g = u >> 1;
                 const float r = ceilf(gm * kL);
                 if (r > r2) {
                     const float f = pow2_down(r2 - r);
@@ -265,108 +296,106 @@ __global__ void __launch_bounds__(kThreads) select_rows_kernel(const BeamArgs a)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) s[i & 3] += fast_exp2(fmaf(x[i], kL, -r2));
+            for (int i = 0; i < kUnit; ++i) s[i & 3] += fast_exp2(fmaf(x[i], kL, -r2));
         }
     }
-
-    // ---- 2. the share's maximum and sum
-    float m_all, r_all;
-    {
-        const float wm = warp_max(best), wr = warp_max(r2);
-        if (lane == 0) {
-            sm.red_m[warp] = wm;
-            sm.red_r[warp] = wr;
-        }
-        sm.top[tid] = best > kNegInf ? ((unsigned long long)ord32(best) << 32) | (unsigned)~best_g
-                                     : (unsigned long long)(kThreads - 1 - tid);
-        if (tid == 0) sm.count = 0;
-        __syncthreads();
-        m_all = sm.red_m[0];
-        r_all = sm.red_r[0];
+    sm.s[tid] = (s[0] + s[1]) + (s[2] + s[3]);
+    sm.r[tid] = r2;
+    unsigned long long top = best > kNegInf ? ((unsigned long long)ord32(best) << 32) | (unsigned)~best_g : 0ull;
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) {
-            m_all = fmaxf(m_all, sm.red_m[i]);
-            r_all = fmaxf(r_all, sm.red_r[i]);
-        }
+    for (int o = 1; o < 4; o <<= 1) {
+        const unsigned long long y = __shfl_xor_sync(0xffffffffu, top, o);
+        top = y > top ? y : top;
     }
-    float mine = (s[0] + s[1]) + (s[2] + s[3]);
+    const bool none = top == 0;
+    if (none) top = (unsigned long long)(kQuads - 1 - (tid >> 2));  // below every group, and different in every quad
+    if ((lane & 3) == 0) sm.top[tid >> 2] = top;
+    if (tid < 2) sm.found[tid] = 0;
+    __syncthreads();
+
+    // ---- 2. the share's maximum; its sum again against that maximum where it is far out
+    float m_all;
+    {
+        const unsigned long long x = sm.top[lane], y = sm.top[lane + 32];
+        const unsigned o = __reduce_max_sync(0xffffffffu, (unsigned)((x > y ? x : y) >> 32));
+        m_all = o ? unord32(o) : kNegInf;
+    }
     const bool far = m_all > kPlainRange || (m_all < -kPlainRange && m_all != kNegInf);
     if (far) {
-        mine = 0.f;
-        for (int g = tid; g < sh.groups; g += kThreads) {
+        float t = 0.f;
+        for (int u = tid; u < sh.units; u += kThreads) {
             uint32_t w[kWords];
-            float x[kGroup];
-            sh.load(g, w);
+            float x[kUnit];
+            sh.load(u, w);
             E::unpack(w, x);
 #pragma unroll
-            for (int i = 0; i < kGroup; ++i) mine += fast_exp2((x[i] - m_all) * kL);
+            for (int i = 0; i < kUnit; ++i) t += fast_exp2((x[i] - m_all) * kL);
         }
-    } else {
-        mine *= pow2_down(r2 - r_all);  // keeps a NaN
-    }
-    {
-        const double ws = warp_sum((double)mine);
-        if (lane == 0) sm.red_s[warp] = ws;
+        sm.s[tid] = t;
+        __syncthreads();
     }
 
-    // ---- 3. the groups at or above the M-th best of the threads' best groups
-    const int M = a.M;
-    const unsigned long long my_top = sm.top[tid];
-    if (rank_of(sm.top, kThreads, my_top) == M - 1) sm.threshold = my_top;
-    __syncthreads();
-    if (tid == 0) {
-        double t = sm.red_s[0];
+    // ---- 3. the threshold: the M-th best of the quads' best groups; meanwhile the last warp adds the sums up
+    if (tid < kQuads) {
+        const unsigned long long key = sm.top[tid];
+        if (rank_of(sm.top, kQuads, key) == M - 1) sm.threshold = key;
+    } else if (warp == kThreads / 32 - 1) {
+        float r = kNegInf;
 #pragma unroll
-        for (int i = 1; i < kThreads / 32; ++i) t += sm.red_s[i];
-        BeamPart out;
-        out.r2 = far ? kInf : r_all;
-        out.m = m_all;
-        out.s = t;
-        a.part[blockIdx.x] = out;
-    }
-    const unsigned long long thr = sm.threshold;
-    if (my_top >= thr && best > kNegInf) {
-        for (int g = tid; g < sh.groups; g += kThreads) {
-            const float v = sm.gmax[g];
-            const unsigned long long key = ((unsigned long long)ord32(v) << 32) | (unsigned)~g;
-            if (key >= thr && v > kNegInf) sm.list[atomicAdd(&sm.count, 1)] = key;
+        for (int i = 0; i < kThreads / 32; ++i) r = fmaxf(r, sm.r[lane + 32 * i]);
+        r = warp_max(r);
+        double t = 0.0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i)  // scaled by exact powers of two (a NaN stays one)
+            t += (double)(far ? sm.s[lane + 32 * i] : sm.s[lane + 32 * i] * pow2_down(sm.r[lane + 32 * i] - r));
+        t = warp_sum(t);
+        if (lane == 0) {
+            BeamPart out;
+            out.r2 = far ? kInf : r;
+            out.m = m_all;
+            out.s = t;
+            a.part[blockIdx.x] = out;
         }
     }
     __syncthreads();
-    int n = sm.count;  // <= M x (groups per thread) <= kListCap
-    if (tid == 0) sm.list[n] = 0;  // an even count for the ranking
+    const unsigned long long thr = sm.threshold;
+    if (!none && top >= thr && !(lane & 1)) {
+        for (int g = tid >> 1; g < groups; g += kThreads / 2) {
+            const float v = gmax[g];
+            const unsigned long long key = ((unsigned long long)ord32(v) << 32) | (unsigned)~g;
+            if (key >= thr && v > kNegInf) list[atomicAdd(&sm.found[0], 1)] = key;
+        }
+    }
     __syncthreads();
+    const int n = sm.found[0];  // <= M x (groups of a quad)
     for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = sm.list[i];
-        const int r = rank_of(sm.list, (n + 1) & ~1, key);
+        const unsigned long long key = list[i];
+        int r = rank_of(list, n & ~1, key);
+        if (n & 1) r += list[n - 1] > key;
         if (r < M) sm.sel[r] = (int)~(unsigned)key;
     }
-    const int n_sel = min(n, M);
-    __syncthreads();  // the list and its count are free again
-    if (tid == 0) sm.count = 0;
     __syncthreads();
 
-    // ---- 4. the tokens of those groups that can be among the M best, ranked
+    // ---- 4. the tokens of the best groups that can be among the M best, ranked
     const unsigned thr_v = (unsigned)(thr >> 32);
-    for (int i = tid; i < n_sel * kGroup; i += kThreads) {
+    for (int i = tid; i < min(n, M) * kGroup; i += kThreads) {
         const int e = sm.sel[i / kGroup] * kGroup + i % kGroup;
         if (e >= sh.len) continue;
         const float v = E::get(sh.p + e);
         const unsigned o = ord32(v);
         if (v > kNegInf && o >= thr_v)
-            sm.list[atomicAdd(&sm.count, 1)] = ((unsigned long long)o << 32) | (unsigned)~(e0 + e);
+            tokens[atomicAdd(&sm.found[1], 1)] = ((unsigned long long)o << 32) | (unsigned)~(e0 + e);
     }
     __syncthreads();
-    n = sm.count;
-    if (tid == 0) sm.list[n] = 0;
-    __syncthreads();
+    const int nt = sm.found[1];
     unsigned long long* out = a.best + (size_t)blockIdx.x * M;
-    for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = sm.list[i];
-        const int r = rank_of(sm.list, (n + 1) & ~1, key);
+    for (int i = tid; i < nt; i += kThreads) {
+        const unsigned long long key = tokens[i];
+        int r = rank_of(tokens, nt & ~1, key);
+        if (nt & 1) r += tokens[nt - 1] > key;
         if (r < M) out[r] = key;
     }
-    if (tid >= n && tid < M) out[tid] = 0;
+    if (tid >= nt && tid < M) out[tid] = 0;
 }
 
 // ---------------------------------------------------------------------------- merge over a group's rows
@@ -383,110 +412,160 @@ __device__ __forceinline__ double unord64(unsigned long long o) {
     return __longlong_as_double((long long)((o >> 63) ? (o & ~(1ull << 63)) : ~o));
 }
 
-// at most M threads pass the threshold, each with its share of the K x parts x M candidates
-constexpr int kMergeCap = kBeamMaxSelect * kBeamMaxCands / kThreads;
+// log2 of a positive normal number, to about 2^-44: 2^e m with m in [sqrt(1/2), sqrt(2)), and the series of
+// ln m = 2 artanh t, t = (m - 1) / (m + 1), |t| < 0.172, cut behind t^13 / 13 (the next term is below 3e-13).  Sixteen
+// 64-bit operations: they are slow on this GPU.
+__device__ __forceinline__ double log2_series(double s) {
+    const long long b = __double_as_longlong(s);
+    int e = (int)((b >> 52) & 0x7ff) - 1023;
+    double m = __longlong_as_double((b & 0x000fffffffffffffll) | 0x3ff0000000000000ll);
+    if (m > 1.4142135623730951) {
+        m *= 0.5;
+        ++e;
+    }
+    const double den = m + 1.0;
+    double inv = (double)__frcp_rn((float)den);
+    inv = inv * (2.0 - den * inv);  // one Newton step: 2^-24 squared
+    const double t = (m - 1.0) * inv, q = t * t;
+    double p = 1.0 / 13.0;
+    p = p * q + 1.0 / 11.0;
+    p = p * q + 1.0 / 9.0;
+    p = p * q + 1.0 / 7.0;
+    p = p * q + 1.0 / 5.0;
+    p = p * q + 1.0 / 3.0;
+    p = p * q + 1.0;
+    return (double)e + 2.8853900817779268 * (t * p);  // 2 / ln 2
+}
+
+struct MergeSmem {
+    alignas(16) Cand top[kQuads];
+    double lse[kBeamMaxBeams];
+    float cum[kBeamMaxBeams];
+    int state[kBeamMaxBeams];  // 0: no continuation, 1: read, 2: finished
+    Cand threshold;
+    int found;
+};
+// Behind it: the K x parts x M candidates, and the numbers of those at or above the threshold.
+inline size_t merge_smem(int total) { return sizeof(MergeSmem) + (size_t)total * (sizeof(Cand) + 4); }
 
 __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a) {
-    __shared__ double lse[kBeamMaxBeams];
-    __shared__ float cum[kBeamMaxBeams];
-    __shared__ int state[kBeamMaxBeams];  // 0: no continuation, 1: read, 2: finished
-    __shared__ Cand top[kThreads];
-    __shared__ Cand list[kMergeCap];
-    __shared__ Cand threshold;
-    __shared__ int count;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x;
+    const int K = a.K, M = a.M, parts = a.parts, total = K * parts * M;
+    Cand* cands = reinterpret_cast<Cand*>(&sm + 1);
+    int* list = reinterpret_cast<int*>(cands + total);
+    if (tid == 0) sm.found = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, n = blockIdx.x;
-    const int K = a.K, M = a.M, parts = a.parts, total = K * parts * M;
 
-    // ---- 1. each row's log-sum-exp from its shares
-    if (tid == 0) count = 0;
-    if (tid < K) {
-        const long long row = (long long)n * K + tid;
+    // ---- 1. each row's log-sum-exp from its shares: a warp per row, a lane per share
+    for (int k = warp; k < K; k += kThreads / 32) {
+        const long long row = (long long)n * K + k;
         const float c = __ldcg(&a.scores[row]);
-        int st = c > kNegInf && c < kInf ? 1 : 0;
-        if (c != c || c == kInf) atomicOr(a.err, kErrBadValue);
-        if (st && a.finished && __ldcg(&a.finished[row])) st = 2;
+        const bool done = a.finished && __ldcg(&a.finished[row]);
+        int st = c > kNegInf && c < kInf ? (done ? 2 : 1) : 0;
+        bool bad = c != c || c == kInf;
         double l = 0.0;
         if (st == 1) {
             const BeamPart* p = a.part + row * parts;
             float m = kNegInf, r = -1e9f;
             bool far = false, nan = false;
-            for (int i = 0; i < parts; ++i) {
-                m = fmaxf(m, __ldcg(&p[i].m));
+            for (int i = lane; i < parts; i += 32) {
                 const float ri = __ldcg(&p[i].r2);
-                if (ri == kInf) far = true;
-                else r = fmaxf(r, ri);
-                nan = nan || __ldcg(&p[i].s) != __ldcg(&p[i].s);
+                const double si = __ldcg(&p[i].s);
+                m = fmaxf(m, __ldcg(&p[i].m));
+                far = far || ri == kInf;
+                r = ri == kInf ? r : fmaxf(r, ri);
+                nan = nan || si != si;
             }
+            m = warp_max(m);
+            r = warp_max(r);
+            far = __any_sync(0xffffffffu, far);
+            nan = __any_sync(0xffffffffu, nan);
             if (nan || m == kInf) {
-                atomicOr(a.err, kErrBadValue);
+                bad = true;
                 st = 0;
             } else if (m == kNegInf) {  // every token is masked
                 st = 0;
             } else if (!far) {
                 double sum = 0.0;
-                for (int i = 0; i < parts; ++i) sum += __ldcg(&p[i].s) * (double)pow2_down(__ldcg(&p[i].r2) - r);
-                l = ((double)r + log2(sum)) / (double)kL;
+                for (int i = lane; i < parts; i += 32) sum += __ldcg(&p[i].s) * (double)pow2_down(__ldcg(&p[i].r2) - r);
+                l = ((double)r + log2_series(warp_sum(sum))) * (1.0 / (double)kL);
             } else {
                 double sum = 0.0;
-                for (int i = 0; i < parts; ++i) {
+                for (int i = lane; i < parts; i += 32) {
                     const float mi = __ldcg(&p[i].m), ri = __ldcg(&p[i].r2);
                     if (mi == kNegInf) continue;
                     const double li = ri == kInf ? (double)mi + log(__ldcg(&p[i].s))
-                                                 : ((double)ri + log2(__ldcg(&p[i].s))) / (double)kL;
+                                                 : ((double)ri + log2_series(__ldcg(&p[i].s))) * (1.0 / (double)kL);
                     sum += exp(li - (double)m);
                 }
-                l = (double)m + log(sum);
+                l = (double)m + log(warp_sum(sum));
             }
         }
-        lse[tid] = l;
-        cum[tid] = c;
-        state[tid] = st;
+        if (lane == 0) {
+            if (bad) atomicOr(a.err, kErrBadValue);
+            sm.lse[k] = l;
+            sm.cum[k] = c;
+            sm.state[k] = st;
+        }
     }
     __syncthreads();
 
-    // ---- 2. every thread's best continuation; the M-th best of them bounds the M-th best of all
-    auto cand = [&](int i) {
-        Cand r = {0ull, 0ull};
-        const int k = i / (parts * M), st = state[k];
+    // ---- 2. the candidates; the M-th best of the quads' best bounds the M-th best of all
+    Cand mine = {0ull, 0ull};
+    for (int i = tid; i < total; i += kThreads) {
+        Cand x = {0ull, 0ull};
+        const int k = i / (parts * M), st = sm.state[k];
         if (st == 1) {
-            const unsigned long long key = __ldcg(&a.best[((long long)n * K * parts) * M + i]);
+            const unsigned long long key = __ldcg(&a.best[(long long)n * total + i]);
             if (key) {
                 const double z = unord32((unsigned)(key >> 32));
-                r.score = ord64((double)cum[k] + (z - lse[k]));
-                r.at = ~(((unsigned long long)k << 32) | ~(unsigned)key);
+                x.score = ord64((double)sm.cum[k] + (z - sm.lse[k]));
+                x.at = ~(((unsigned long long)k << 32) | ~(unsigned)key);
             }
         } else if (st == 2 && i == k * parts * M) {
-            r.score = ord64((double)cum[k]);
-            r.at = ~(((unsigned long long)k << 32) | (unsigned)a.pad_token);
+            x.score = ord64((double)sm.cum[k]);
+            x.at = ~(((unsigned long long)k << 32) | (unsigned)a.pad_token);
         }
-        return r;
-    };
-    Cand mine = {0ull, (unsigned long long)(kThreads - 1 - tid)};  // none, but different in every thread
-    for (int i = tid; i < total; i += kThreads) {
-        const Cand x = cand(i);
-        if (x.score && x.above(mine)) mine = x;
+        cands[i] = x;
+        if (x.above(mine)) mine = x;
     }
-    top[tid] = mine;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        Cand y;
+        y.score = __shfl_xor_sync(0xffffffffu, mine.score, o);
+        y.at = __shfl_xor_sync(0xffffffffu, mine.at, o);
+        if (y.above(mine)) mine = y;
+    }
+    if (!mine.score) mine.at = (unsigned long long)(kQuads - 1 - (tid >> 2));  // none, but different in every quad
+    if ((lane & 3) == 0) sm.top[tid >> 2] = mine;
     __syncthreads();
-    int r = 0;
-    for (int i = 0; i < kThreads; ++i) r += top[i].above(mine);
-    if (r == M - 1) threshold = mine;
+    if (tid < kQuads) {
+        const Cand x = sm.top[tid];
+        int r = 0;
+#pragma unroll 8
+        for (int i = 0; i < kQuads; ++i) r += sm.top[i].above(x);
+        if (r == M - 1) sm.threshold = x;
+    }
     __syncthreads();
-    const Cand thr = threshold;
-    if (!thr.above(mine) && mine.score) {
+    const Cand thr = sm.threshold;
+    if (mine.score && !thr.above(mine)) {
         for (int i = tid; i < total; i += kThreads) {
-            const Cand x = cand(i);
-            if (x.score && !thr.above(x)) list[atomicAdd(&count, 1)] = x;
+            const Cand x = cands[i];
+            if (x.score && !thr.above(x)) list[atomicAdd(&sm.found, 1)] = i;
         }
     }
     __syncthreads();
-    const int found = count;
+
+    // ---- 3. ranked by counting
+    const int found = sm.found;
     for (int i = tid; i < found; i += kThreads) {
-        const Cand x = list[i];
+        const Cand x = cands[list[i]];
         int q = 0;
-        for (int j = 0; j < found; ++j) q += list[j].above(x);
+#pragma unroll 4
+        for (int j = 0; j < found; ++j) q += cands[list[j]].above(x);
         if (q < M) {
             const unsigned long long at = ~x.at;
             a.out_scores[(long long)n * M + q] = (float)unord64(x.score);
@@ -501,6 +580,19 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     }
 }
 
+// Shared memory that a kernel may be launched with, raised once per device and thread as calls ask for more.
+cudaError_t allow_smem(const void* kernel, int which, size_t bytes) {
+    static thread_local size_t allowed[64][4] = {};
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && allowed[dev][which] >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) allowed[dev][which] = bytes;
+    return e;
+}
+
 }  // namespace
 
 cudaError_t beam_plan(int N, int K, int V, int M, BeamPlan* plan) {
@@ -509,7 +601,7 @@ cudaError_t beam_plan(int N, int K, int V, int M, BeamPlan* plan) {
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const long long rows = (long long)N * K;
-    // shares of a row: enough to give every SM four CTAs, but not below 4096 tokens (a thread's one step)
+    // shares of a row: as many as run at once (four CTAs an SM), but none below 4096 tokens (one step of a thread)
     long long parts = rows > 0 ? (4ll * sms) / rows : 1;
     const long long fine = V / 4096;
     if (parts > fine) parts = fine;
@@ -536,14 +628,20 @@ cudaError_t beam_select_launch(const BeamArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)units);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = select_smem(a.part_len, a.M);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = a.dtype == kDtF32    ? cudaLaunchKernelEx(&cfg, select_rows_kernel<kDtF32>, a)
-                    : a.dtype == kDtBf16 ? cudaLaunchKernelEx(&cfg, select_rows_kernel<kDtBf16>, a)
-                                                  : cudaLaunchKernelEx(&cfg, select_rows_kernel<kDtF16>, a);
+    void (*rows)(const BeamArgs) = a.dtype == kDtF32    ? select_rows_kernel<kDtF32>
+                                   : a.dtype == kDtBf16 ? select_rows_kernel<kDtBf16>
+                                                        : select_rows_kernel<kDtF16>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(rows), a.dtype, cfg.dynamicSmemBytes);
     if (e != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&cfg, rows, a)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)a.N);
+    cfg.dynamicSmemBytes = merge_smem(a.K * a.parts * a.M);
+    if ((e = allow_smem(reinterpret_cast<const void*>(select_merge_kernel), 3, cfg.dynamicSmemBytes)) != cudaSuccess)
+        return e;
     return cudaLaunchKernelEx(&cfg, select_merge_kernel, a);
 }
 
