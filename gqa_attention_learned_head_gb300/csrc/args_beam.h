@@ -10,13 +10,12 @@ constexpr int kBeamMaxBeams = 32;    // K
 constexpr int kBeamMaxSelect = 64;   // M
 constexpr int kBeamMaxPart = 262144;  // tokens of one row that one CTA reads at most
 
-constexpr int kBeamMaxCands = 8192;  // K x shares of a row x M: candidates that meet in the merge
+constexpr int kBeamMaxCands = 4096;  // K x shares of a row x M: candidates that meet in the merge
 
-// One CTA's share of a row: its largest logit m and the sum of exponentials, s = sum 2^(x L - r2) with L
-// the float log2(e), or, where r2 is +inf (|m| above 2^20), s = sum e^(x - m).
+// One CTA's share of a row: its largest logit m and its sum of exponentials, hi + lo = sum 2^(x L - r2) with L the
+// float log2(e), or, where r2 is +inf (|m| above 2^20), sum e^(x - m).
 struct BeamPart {
-    float r2, m;
-    double s;
+    float r2, m, hi, lo;
 };
 struct BeamArgs {
     const void* logits;         // [N * K rows, V], rows row_stride elements apart

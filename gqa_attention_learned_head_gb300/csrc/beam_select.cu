@@ -4,11 +4,11 @@
 // Mathematics.  score(k, v) = c_k + (z_kv - lse_k), lse_k = ln sum_u e^(z_ku).  Within a row the order of
 // the scores is that of the logits, so one pass over a row gives both its sum of exponentials and its M best
 // tokens, and only M candidates a row meet the rows of the group.
-//   Sum.  Every thread keeps sums of 2^(x L - r) (L = log2 e in 32 bits) against an integer r at or above its
+//   Sum.  Every thread keeps sums of 2^(x L - r) (L = log2 e in 32 bits) against an integer r near its
 //   largest x L: moving to another r multiplies by a power of two, which is exact, so how a row is cut
 //   changes nothing but the order of additions.  Threads hold 32-bit sums of a few hundred terms, everything
-//   above that is in 64 bits: the scores of two beams may lie next to each other.  lse = (r + log2 s) / L
-//   with the same rounded L, so its rounding cancels to first order.  Where the largest logit is beyond
+//   above that is in pairs of floats (48 bits): the scores of two beams may lie next to each other.
+//   lse = (r + log2 s) / L with the same rounded L, so its rounding cancels to first order.  Where the largest logit is beyond
 //   +-2^20 (rows of nothing but a type's lowest value) the share is read again and summed as e^(x - m).
 //   Best tokens.  The row is cut into groups of 32 consecutive tokens whose maxima stay in shared memory.  The M
 //   best tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there
@@ -36,6 +36,7 @@ static_assert(kQuads >= kBeamMaxSelect, "the threshold needs M maxima");
 constexpr float kL = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kInf = __builtin_huge_valf();
+constexpr float kSlack = 16.f;  // log2 units that a thread's largest exponential may be above its reference
 constexpr float kPlainRange = 1048576.f;  // 2^20: largest |logit| whose x L - r keeps its fraction's worth
 
 // Order of a float as an unsigned number (-0 taken as +0): larger value, larger number; every float's is > 0.
@@ -58,7 +59,7 @@ struct Elem<kDtF32> {
     using T = float;
     static constexpr unsigned kNone = 0xFF800000u;  // -inf
     __device__ static float get(const T* p) { return __ldcg(p); }
-    __device__ static void unpack(const uint32_t (&w)[16], float (&x)[16]) {
+    __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(w[i]);
     }
@@ -68,7 +69,7 @@ struct Elem<kDtBf16> {
     using T = unsigned short;
     static constexpr unsigned kNone = 0xFF80u;
     __device__ static float get(const T* p) { return __uint_as_float((unsigned)__ldcg(p) << 16); }
-    __device__ static void unpack(const uint32_t (&w)[8], float (&x)[16]) {
+    __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             x[2 * i] = __uint_as_float(w[i] << 16);
@@ -81,7 +82,7 @@ struct Elem<kDtF16> {
     using T = unsigned short;
     static constexpr unsigned kNone = 0xFC00u;
     __device__ static float get(const T* p) { return __half2float(__ushort_as_half(__ldcg(p))); }
-    __device__ static void unpack(const uint32_t (&w)[8], float (&x)[16]) {
+    __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -91,14 +92,20 @@ struct Elem<kDtF16> {
     }
 };
 
-// 32 bytes from a 32-byte boundary: one whole sector a thread.
-__device__ __forceinline__ void load32(const void* p, uint32_t* r) {
+// 32 bytes from a 32-byte boundary: one whole sector.  The first form leaves no copy in L1, the second does (its
+// neighbour reads the sector too).
+__device__ __forceinline__ void load_sector(const void* p, uint32_t* r) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
+__device__ __forceinline__ void load_shared_sector(const void* p, uint32_t* r) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p));
+}
 
-// A row's share: where it starts, and which of its units can be read in whole pieces.
+// A row's share: where it starts, and which of its units can be read in whole sectors.
 template <int DT>
 struct Share {
     using E = Elem<DT>;
@@ -106,91 +113,101 @@ struct Share {
     static constexpr int kWords = kUnit * (int)sizeof(T) / 4;  // 32-bit words of a unit
     const T* p;      // first token of the share
     int len, units;  // tokens, units (the last may be partial)
-    int off;         // bytes from the 16-byte boundary at or below p (0..15), the same for every unit
-    bool sectors;    // units start at 32-byte boundaries
-    int lo, hi;      // units [lo, hi) are whole and their 16-byte pieces lie inside the tensor
+    int off;         // bytes from the sector boundary at or below p, the same for every unit
+    int lo, hi;      // units [lo, hi) are whole and the sectors they touch lie inside the tensor
 
     __device__ void set(const T* tensor, const T* tensor_end, const T* first, int n) {
         p = first;
         len = n;
         units = (n + kUnit - 1) / kUnit;
-        off = (int)(reinterpret_cast<uintptr_t>(p) & 15);
-        sectors = (reinterpret_cast<uintptr_t>(p) & 31) == 0;
+        off = (int)(reinterpret_cast<uintptr_t>(p) & 31);
         hi = n / kUnit;
         lo = 0;
-        if (off) {  // a unit's pieces then start before it and end behind it
+        if (off) {  // a unit's sectors then start before it and end behind it, by less than a unit
             const char* c = reinterpret_cast<const char*>(p) - off;
             if (c < reinterpret_cast<const char*>(tensor)) lo = 1;
-            if (hi > 0 && c + hi * (kWords * 4) + 16 > reinterpret_cast<const char*>(tensor_end)) --hi;
+            if (hi > 0 && c + hi * (kWords * 4) + 32 > reinterpret_cast<const char*>(tensor_end)) --hi;
         }
     }
-    // Unit u's values as words: whole sectors, or 16-byte pieces, shifted together if the row is not aligned to
-    // them; token by token at the tensor's edges and past the share's end (-inf there).  The thread that holds a
-    // token, and so the order of every sum, does not depend on where the row starts.
-    __device__ void load(int u, uint32_t (&w)[kWords]) const {
+    // Unit u's values as words: its sectors, or the sectors around it, shifted; token by token at the tensor's edges
+    // and past the share's end (-inf there).  The thread that holds a token, and so the order of every sum, does
+    // not depend on where the row starts.
+    template <bool ALIGNED>
+    __device__ void load(int u, uint32_t* w) const {
+        const char* c = reinterpret_cast<const char*>(p) - off + (size_t)u * (kWords * 4);
         if (u >= lo && u < hi) {
-            const char* c = reinterpret_cast<const char*>(p) - off + (size_t)u * (kWords * 4);
-            const uint4* v = reinterpret_cast<const uint4*>(c);
-            if (sectors) {
+            if constexpr (ALIGNED) {
 #pragma unroll
-                for (int i = 0; i < kWords / 8; ++i) load32(c + 32 * i, &w[8 * i]);
-            } else if (off == 0) {
-#pragma unroll
-                for (int i = 0; i < kWords / 4; ++i) {
-                    const uint4 q = v[i];
-                    w[4 * i] = q.x;
-                    w[4 * i + 1] = q.y;
-                    w[4 * i + 2] = q.z;
-                    w[4 * i + 3] = q.w;
-                }
+                for (int i = 0; i < kWords / 8; ++i) load_sector(c + 32 * i, &w[8 * i]);
             } else {
-                uint32_t r[kWords + 4];
 #pragma unroll
-                for (int i = 0; i < kWords / 4 + 1; ++i) {
-                    const uint4 q = v[i];
-                    r[4 * i] = q.x;
-                    r[4 * i + 1] = q.y;
-                    r[4 * i + 2] = q.z;
-                    r[4 * i + 3] = q.w;
-                }
-                if (off & 8) {
-#pragma unroll
-                    for (int i = 0; i < kWords + 2; ++i) r[i] = r[i + 2];
-                }
-                if (off & 4) {
-#pragma unroll
-                    for (int i = 0; i < kWords + 1; ++i) r[i] = r[i + 1];
-                }
-                if constexpr (sizeof(T) == 4) {
-#pragma unroll
-                    for (int i = 0; i < kWords; ++i) w[i] = r[i];
-                } else {
-                    const int bits = 8 * (off & 3);
-#pragma unroll
-                    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(r[i], r[i + 1], bits);
-                }
+                for (int i = 0; i < kWords / 8 + 1; ++i) load_shared_sector(c + 32 * i, &w[8 * i]);
             }
         } else {
+            uint32_t* to = w + (ALIGNED ? 0 : 8);  // as if shifted by a whole sector: see settle
 #pragma unroll
             for (int i = 0; i < kWords; ++i) {
                 if constexpr (sizeof(T) == 4) {
                     const int e = u * kUnit + i;
-                    w[i] = e < len ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(p) + e)) : E::kNone;
+                    to[i] = e < len ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(p) + e)) : E::kNone;
                 } else {
                     const int e = u * kUnit + 2 * i;
                     const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
                     const unsigned a = e < len ? (unsigned)__ldcg(h + e) : E::kNone;
                     const unsigned b = e + 1 < len ? (unsigned)__ldcg(h + e + 1) : E::kNone;
-                    w[i] = a | (b << 16);
+                    to[i] = a | (b << 16);
                 }
             }
         }
     }
+    // Moves what load<false> brought to the front: w[0 .. kWords) are the unit's words.
+    __device__ void settle(int u, uint32_t (&w)[kWords + 8]) const {
+        if (u >= lo && u < hi) {
+            if (off & 16) {
+#pragma unroll
+                for (int i = 0; i < kWords + 4; ++i) w[i] = w[i + 4];
+            }
+            if (off & 8) {
+#pragma unroll
+                for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
+            }
+            if (off & 4) {
+#pragma unroll
+                for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
+            }
+            if constexpr (sizeof(T) == 2) {
+                if (off & 2) {
+#pragma unroll
+                    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = w[i + 8];
+        }
+    }
 };
 
-__device__ __forceinline__ double warp_sum(double v) {
+// A number as the unevaluated sum of two floats (48 bits): the 64-bit unit of this GPU takes some hundred cycles an
+// operation.  two_sum and its use here are Knuth's error-free addition.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two two_sum(float a, float b) {
+    const float s = a + b, t = s - a;
+    return Two{s, (a - (s - t)) + (b - t)};
+}
+__device__ __forceinline__ Two add(Two a, Two b) {
+    const Two s = two_sum(a.hi, b.hi);
+    const float lo = s.lo + (a.lo + b.lo), hi = s.hi + lo;
+    return Two{hi, lo - (hi - s.hi)};
+}
+__device__ __forceinline__ Two warp_sum(Two v, int lanes) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        if (o >= lanes) break;
+        v = add(v, Two{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+    }
     return v;
 }
 __device__ __forceinline__ float warp_max(float v) {
@@ -211,6 +228,64 @@ __device__ __forceinline__ int rank_of(const unsigned long long* keys, int n, un
     return r;
 }
 
+// What a thread gathers on its way through a share: sum of 2^(x L - r2), the best group it met and its maximum.
+struct Gather {
+    float2 s2[2];
+    float r2, best;
+    int best_g;
+};
+
+// One pass over the share; every group's maximum goes to gmax.  A group is two neighbouring threads' units.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ void stream(const Share<DT>& sh, float* gmax, Gather& t) {
+    using E = Elem<DT>;
+    constexpr int kWords = Share<DT>::kWords, kHeld = kWords + (ALIGNED ? 0 : 8);
+    constexpr int kBatch = ALIGNED ? 32 / kWords : (kWords == 16 ? 1 : 2);  // units loaded together
+    const int tid = threadIdx.x;
+    for (int u0 = tid; u0 - (tid & 31) < sh.units; u0 += kThreads * kBatch) {  // whole warps
+        uint32_t w[kBatch][kHeld];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = u0 + b * kThreads;
+            if (u < sh.units) {
+                sh.template load<ALIGNED>(u, w[b]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) w[b][i] = sizeof(typename E::T) == 4 ? E::kNone : E::kNone * 0x10001u;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int u = u0 + b * kThreads;
+            float x[kUnit];
+            if constexpr (!ALIGNED) sh.settle(u, w[b]);
+            E::unpack(w[b], x);
+            float m4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
+            float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
+            if (!(tid & 1) && u < sh.units) gmax[u >> 1] = gm;
+            t.best_g = gm > t.best ? u >> 1 : t.best_g;
+            t.best = fmaxf(t.best, gm);
+            // sums up to 2^kSlack times the reference's lose nothing, so it moves once or twice a row, not with
+            // every new maximum (in a warp, one thread or another meets one nearly every time)
+            if (gm * kL > t.r2 + kSlack) {
+                const float r = ceilf(gm * kL), f = pow2_down(t.r2 - r);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) t.s2[i] = make_float2(t.s2[i].x * f, t.s2[i].y * f);
+                t.r2 = r;
+            }
+            const float2 l2 = make_float2(kL, kL), neg = make_float2(-t.r2, -t.r2);
+#pragma unroll
+            for (int i = 0; i < kUnit / 2; ++i) {
+                const float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), l2, neg);
+                t.s2[i & 1] = fadd2(t.s2[i & 1], make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+            }
+        }
+    }
+}
+
 struct SelectSmem {
     alignas(16) unsigned long long top[kQuads];  // the quads' best groups
     float s[kThreads], r[kThreads];              // the threads' sums and references
@@ -225,7 +300,7 @@ __host__ __device__ inline int list_cap(int groups, int M) {  // a quad has two 
 }
 __host__ __device__ inline size_t select_smem(int part_len, int M) {
     const int groups = groups_of(part_len);
-    return sizeof(SelectSmem) + ((size_t)list_cap(groups, M) + M * kGroup + 2) * 8 + (size_t)groups * 4;
+    return sizeof(SelectSmem) + ((size_t)list_cap(groups, M) + M * kGroup + 2) * 8 + (size_t)((groups + 3) & ~3) * 4;
 }
 
 template <int DT>
@@ -233,7 +308,6 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     using E = Elem<DT>;
     using T = typename E::T;
     constexpr int kWords = Share<DT>::kWords;
-    constexpr int kBatch = 32 / kWords;  // units loaded together: 128 bytes a thread
     extern __shared__ __align__(16) unsigned char smem_raw[];
     SelectSmem& sm = *reinterpret_cast<SelectSmem*>(smem_raw);
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -257,58 +331,19 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     unsigned long long* tokens = list + list_cap(groups_of(a.part_len), M);
     float* gmax = reinterpret_cast<float*>(tokens + M * kGroup + 2);
 
-    // ---- 1. one pass over the share: sums, and every group's maximum.  A group is two neighbouring threads' units.
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    float r2 = -1e9f, best = kNegInf;
-    int best_g = 0;
-    for (int u0 = tid; u0 - lane < sh.units; u0 += kThreads * kBatch) {  // whole warps
-        uint32_t w[kBatch][kWords];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int u = u0 + b * kThreads;
-            if (u < sh.units) {
-                sh.load(u, w[b]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kWords; ++i) w[b][i] = sizeof(T) == 4 ? E::kNone : E::kNone * 0x10001u;
-            }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int u = u0 + b * kThreads;
-            float x[kUnit];
-            E::unpack(w[b], x);
-            float m4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
-            float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
-            if (!(tid & 1) && u < sh.units) gmax[u >> 1] = gm;
-            if (gm > best) {
-                best = gm;
-                best_g = u >> 1;
-                const float r = ceilf(gm * kL);
-                if (r > r2) {
-                    const float f = pow2_down(r2 - r);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s[i] *= f;
-                    r2 = r;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i) s[i & 3] += fast_exp2(fmaf(x[i], kL, -r2));
-        }
-    }
-    sm.s[tid] = (s[0] + s[1]) + (s[2] + s[3]);
-    sm.r[tid] = r2;
-    unsigned long long top = best > kNegInf ? ((unsigned long long)ord32(best) << 32) | (unsigned)~best_g : 0ull;
+    // ---- 1. one pass over the share
+    Gather t = {{make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, -1e9f, kNegInf, 0};
+    if (sh.off == 0) stream<DT, true>(sh, gmax, t);
+    else stream<DT, false>(sh, gmax, t);
+    sm.s[tid] = (t.s2[0].x + t.s2[0].y) + (t.s2[1].x + t.s2[1].y);
+    sm.r[tid] = t.r2;
+    unsigned long long top = t.best > kNegInf ? ((unsigned long long)ord32(t.best) << 32) | (unsigned)~t.best_g : 0ull;
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
         const unsigned long long y = __shfl_xor_sync(0xffffffffu, top, o);
         top = y > top ? y : top;
     }
-    const bool none = top == 0;
-    if (none) top = (unsigned long long)(kQuads - 1 - (tid >> 2));  // below every group, and different in every quad
+    if (top == 0) top = (unsigned long long)(kQuads - 1 - (tid >> 2));  // below every group, and different in every quad
     if ((lane & 3) == 0) sm.top[tid >> 2] = top;
     if (tid < 2) sm.found[tid] = 0;
     __syncthreads();
@@ -322,16 +357,21 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     }
     const bool far = m_all > kPlainRange || (m_all < -kPlainRange && m_all != kNegInf);
     if (far) {
-        float t = 0.f;
+        float sum = 0.f;
         for (int u = tid; u < sh.units; u += kThreads) {
-            uint32_t w[kWords];
+            uint32_t w[kWords + 8];
             float x[kUnit];
-            sh.load(u, w);
+            if (sh.off == 0) {
+                sh.template load<true>(u, w);
+            } else {
+                sh.template load<false>(u, w);
+                sh.settle(u, w);
+            }
             E::unpack(w, x);
 #pragma unroll
-            for (int i = 0; i < kUnit; ++i) t += fast_exp2((x[i] - m_all) * kL);
+            for (int i = 0; i < kUnit; ++i) sum += fast_exp2((x[i] - m_all) * kL);
         }
-        sm.s[tid] = t;
+        sm.s[tid] = sum;
         __syncthreads();
     }
 
@@ -344,26 +384,36 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
 #pragma unroll
         for (int i = 0; i < kThreads / 32; ++i) r = fmaxf(r, sm.r[lane + 32 * i]);
         r = warp_max(r);
-        double t = 0.0;
+        Two sum = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i)  // scaled by exact powers of two (a NaN stays one)
-            t += (double)(far ? sm.s[lane + 32 * i] : sm.s[lane + 32 * i] * pow2_down(sm.r[lane + 32 * i] - r));
-        t = warp_sum(t);
+        for (int i = 0; i < kThreads / 32; ++i) {  // scaled by exact powers of two (a NaN stays one)
+            const float x = far ? sm.s[lane + 32 * i] : sm.s[lane + 32 * i] * pow2_down(sm.r[lane + 32 * i] - r);
+            sum = add(sum, Two{x, 0.f});
+        }
+        sum = warp_sum(sum, 32);
         if (lane == 0) {
             BeamPart out;
             out.r2 = far ? kInf : r;
             out.m = m_all;
-            out.s = t;
+            out.hi = sum.hi;
+            out.lo = sum.lo;
             a.part[blockIdx.x] = out;
         }
     }
     __syncthreads();
     const unsigned long long thr = sm.threshold;
-    if (!none && top >= thr && !(lane & 1)) {
-        for (int g = tid >> 1; g < groups; g += kThreads / 2) {
-            const float v = gmax[g];
-            const unsigned long long key = ((unsigned long long)ord32(v) << 32) | (unsigned)~g;
-            if (key >= thr && v > kNegInf) list[atomicAdd(&sm.found[0], 1)] = key;
+    {
+        const float thr_f = (thr >> 32) ? unord32((unsigned)(thr >> 32)) : kNegInf;
+        for (int g0 = 4 * tid; g0 < groups; g0 += 4 * kThreads) {
+            const float4 v4 = *reinterpret_cast<const float4*>(gmax + g0);
+            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (v[i] >= thr_f && v[i] > kNegInf && g0 + i < groups) {
+                    const unsigned long long key = ((unsigned long long)ord32(v[i]) << 32) | (unsigned)~(g0 + i);
+                    if (key >= thr) list[atomicAdd(&sm.found[0], 1)] = key;
+                }
+            }
         }
     }
     __syncthreads();
@@ -399,85 +449,94 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
 }
 
 // ---------------------------------------------------------------------------- merge over a group's rows
-// Order of a continuation: its score's order, then ~(beam, token).
-struct Cand {
-    unsigned long long score, at;
-    __device__ bool above(const Cand& o) const { return score > o.score || (score == o.score && at > o.at); }
-};
-__device__ __forceinline__ unsigned long long ord64(double x) {
-    const unsigned long long b = (unsigned long long)__double_as_longlong(x + 0.0);
-    return (b >> 63) ? ~b : (b | (1ull << 63));
-}
-__device__ __forceinline__ double unord64(unsigned long long o) {
-    return __longlong_as_double((long long)((o >> 63) ? (o & ~(1ull << 63)) : ~o));
+// Order of a score hi + lo as an unsigned number; every score's is above 0.
+__device__ __forceinline__ unsigned long long ord_two(Two x) {
+    return ((unsigned long long)ord32(x.hi) << 32) | ord32(fabsf(x.hi) < kInf ? x.lo : 0.f);
 }
 
-// log2 of a positive normal number, to about 2^-44: 2^e m with m in [sqrt(1/2), sqrt(2)), and the series of
-// ln m = 2 artanh t, t = (m - 1) / (m + 1), |t| < 0.172, cut behind t^13 / 13 (the next term is below 3e-13).  Sixteen
-// 64-bit operations: they are slow on this GPU.
-__device__ __forceinline__ double log2_series(double s) {
-    const long long b = __double_as_longlong(s);
-    int e = (int)((b >> 52) & 0x7ff) - 1023;
-    double m = __longlong_as_double((b & 0x000fffffffffffffll) | 0x3ff0000000000000ll);
-    if (m > 1.4142135623730951) {
-        m *= 0.5;
-        ++e;
-    }
-    const double den = m + 1.0;
-    double inv = (double)__frcp_rn((float)den);
-    inv = inv * (2.0 - den * inv);  // one Newton step: 2^-24 squared
-    const double t = (m - 1.0) * inv, q = t * t;
-    double p = 1.0 / 13.0;
-    p = p * q + 1.0 / 11.0;
-    p = p * q + 1.0 / 9.0;
-    p = p * q + 1.0 / 7.0;
-    p = p * q + 1.0 / 5.0;
-    p = p * q + 1.0 / 3.0;
-    p = p * q + 1.0;
-    return (double)e + 2.8853900817779268 * (t * p);  // 2 / ln 2
+// (r + log2 s) / kL for an integer r, a positive s = hi + lo and kL = L as rounded: to about 2e-9 of the logarithm.
+// s = 2^e m with m in [sqrt(1/2), sqrt(2)), n = m - 1, and the series of ln m = 2 artanh t, t = n / (n + 2), |t| < 0.172,
+// cut behind t^9 / 9 (the next term is below 4e-10); its leading terms carry a second float.
+__device__ __forceinline__ Two natural_log(float r, Two s) {
+    const int b = __float_as_int(s.hi);
+    int e = (b >> 23) - 127;
+    if ((b & 0x7fffff) > 0x3504f3) ++e;  // above sqrt(2): half of it
+    const float scale = __int_as_float((127 - e) << 23);
+    const float nh = s.hi * scale - 1.f, nl = s.lo * scale;  // exact
+    const float den = nh + 2.f;
+    const float th = __fdividef(nh, den);
+    const float tl = __fdividef(fmaf(-th, nh, fmaf(-2.f, th, nh)) + nl * (1.f - th), den);
+    const float q = th * th;
+    float p = fmaf(q, 1.f / 9.f, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    constexpr float kCh = 2.885390043258667f;          // 2 / ln 2 as two floats
+    constexpr float kCl = 3.8519259e-08f;
+    const float ph = kCh * th;
+    const float pl = fmaf(kCh, th, -ph) + (fmaf(kCh, tl, kCl * th) + ph * q * p);
+    const Two l2 = add(two_sum(r + (float)e, ph), Two{pl, 0.f});
+    constexpr double kInv = 1.0 / (double)kL;          // as two floats
+    constexpr float kIh = (float)kInv, kIl = (float)(kInv - (double)kIh);
+    const float h = l2.hi * kIh;
+    return add(Two{h, fmaf(l2.hi, kIh, -h)}, Two{fmaf(l2.hi, kIl, l2.lo * kIh), 0.f});
+}
+__device__ __forceinline__ Two to_two(double x) {
+    const float hi = (float)x;
+    return Two{hi, (float)(x - (double)hi)};
 }
 
 struct MergeSmem {
-    alignas(16) Cand top[kQuads];
-    double lse[kBeamMaxBeams];
+    alignas(16) unsigned long long top[kQuads];  // the quads' best scores' orders, 0: none
+    Two lse[kBeamMaxBeams];
     float cum[kBeamMaxBeams];
     int state[kBeamMaxBeams];  // 0: no continuation, 1: read, 2: finished
-    Cand threshold;
+    unsigned long long threshold;
     int found;
 };
-// Behind it: the K x parts x M candidates, and the numbers of those at or above the threshold.
-inline size_t merge_smem(int total) { return sizeof(MergeSmem) + (size_t)total * (sizeof(Cand) + 4); }
+// Behind it: score order and (beam, token) of the K x parts x M candidates, then of those at or above the threshold.
+inline size_t merge_smem(int total) { return sizeof(MergeSmem) + (size_t)((total + 1) & ~1) * 32; }
 
 __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x;
-    const int K = a.K, M = a.M, parts = a.parts, total = K * parts * M;
-    Cand* cands = reinterpret_cast<Cand*>(&sm + 1);
-    int* list = reinterpret_cast<int*>(cands + total);
+    const int K = a.K, M = a.M, parts = a.parts, per_row = parts * M, total = K * per_row;
+    unsigned long long* score = reinterpret_cast<unsigned long long*>(&sm + 1);
+    unsigned long long* at = score + ((total + 1) & ~1);
+    unsigned long long* list_score = at + ((total + 1) & ~1);
+    unsigned long long* list_at = list_score + ((total + 1) & ~1);
     if (tid == 0) sm.found = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // the first candidates are on their way while the rows' sums are put together (those of rows that were not read
+    // hold anything and are not looked at)
+    constexpr int kAhead = 4;
+    const unsigned long long* best = a.best + (long long)n * total;
+    unsigned long long ahead[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < total ? __ldcg(&best[tid + j * kThreads]) : 0ull;
 
     // ---- 1. each row's log-sum-exp from its shares: a warp per row, a lane per share
     for (int k = warp; k < K; k += kThreads / 32) {
         const long long row = (long long)n * K + k;
         const float c = __ldcg(&a.scores[row]);
         const bool done = a.finished && __ldcg(&a.finished[row]);
+        const BeamPart* p = a.part + row * parts;
+        const float4 own = lane < parts ? __ldcg(reinterpret_cast<const float4*>(p + lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto get = [&](int i) { return i == lane ? own : __ldcg(reinterpret_cast<const float4*>(p + i)); };
         int st = c > kNegInf && c < kInf ? (done ? 2 : 1) : 0;
         bool bad = c != c || c == kInf;
-        double l = 0.0;
+        Two l = {0.f, 0.f};
         if (st == 1) {
-            const BeamPart* p = a.part + row * parts;
             float m = kNegInf, r = -1e9f;
             bool far = false, nan = false;
             for (int i = lane; i < parts; i += 32) {
-                const float ri = __ldcg(&p[i].r2);
-                const double si = __ldcg(&p[i].s);
-                m = fmaxf(m, __ldcg(&p[i].m));
-                far = far || ri == kInf;
-                r = ri == kInf ? r : fmaxf(r, ri);
-                nan = nan || si != si;
+                const float4 x = get(i);
+                m = fmaxf(m, x.y);
+                far = far || x.x == kInf;
+                r = x.x == kInf ? r : fmaxf(r, x.x);
+                nan = nan || x.z != x.z;
             }
             m = warp_max(m);
             r = warp_max(r);
@@ -489,19 +548,25 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
             } else if (m == kNegInf) {  // every token is masked
                 st = 0;
             } else if (!far) {
-                double sum = 0.0;
-                for (int i = lane; i < parts; i += 32) sum += __ldcg(&p[i].s) * (double)pow2_down(__ldcg(&p[i].r2) - r);
-                l = ((double)r + log2_series(warp_sum(sum))) * (1.0 / (double)kL);
-            } else {
+                Two sum = {0.f, 0.f};
+                for (int i = lane; i < parts; i += 32) {
+                    const float4 x = get(i);
+                    const float f = pow2_down(x.x - r);
+                    sum = add(sum, Two{x.z * f, x.w * f});
+                }
+                l = natural_log(r, warp_sum(sum, parts));
+            } else {  // shares far out: in 64 bits
                 double sum = 0.0;
                 for (int i = lane; i < parts; i += 32) {
-                    const float mi = __ldcg(&p[i].m), ri = __ldcg(&p[i].r2);
-                    if (mi == kNegInf) continue;
-                    const double li = ri == kInf ? (double)mi + log(__ldcg(&p[i].s))
-                                                 : ((double)ri + log2_series(__ldcg(&p[i].s))) * (1.0 / (double)kL);
+                    const float4 x = get(i);
+                    if (x.y == kNegInf) continue;
+                    const double s = (double)x.z + (double)x.w;
+                    const double li = x.x == kInf ? (double)x.y + log(s) : ((double)x.x + log2(s)) / (double)kL;
                     sum += exp(li - (double)m);
                 }
-                l = (double)m + log(warp_sum(sum));
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                l = to_two((double)m + log(sum));
             }
         }
         if (lane == 0) {
@@ -513,64 +578,87 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     }
     __syncthreads();
 
-    // ---- 2. the candidates; the M-th best of the quads' best bounds the M-th best of all
-    Cand mine = {0ull, 0ull};
-    for (int i = tid; i < total; i += kThreads) {
-        Cand x = {0ull, 0ull};
-        const int k = i / (parts * M), st = sm.state[k];
-        if (st == 1) {
-            const unsigned long long key = __ldcg(&a.best[(long long)n * total + i]);
-            if (key) {
-                const double z = unord32((unsigned)(key >> 32));
-                x.score = ord64((double)sm.cum[k] + (z - sm.lse[k]));
-                x.at = ~(((unsigned long long)k << 32) | ~(unsigned)key);
-            }
-        } else if (st == 2 && i == k * parts * M) {
-            x.score = ord64((double)sm.cum[k]);
-            x.at = ~(((unsigned long long)k << 32) | (unsigned)a.pad_token);
+    // ---- 2. the candidates; the M-th best of the quads' best scores bounds the M-th best of all
+    unsigned long long mine = 0;
+    int j = 0;
+#pragma unroll 1
+    for (int i = tid; i < total; i += kThreads, ++j) {
+        unsigned long long key = ahead[0], x = 0, where = 0;
+        if (j < kAhead) {
+#pragma unroll
+            for (int q = 1; q < kAhead; ++q) key = j == q ? ahead[q] : key;
+        } else {
+            key = __ldcg(&best[i]);
         }
-        cands[i] = x;
-        if (x.above(mine)) mine = x;
+        const int k = i / per_row, st = sm.state[k];
+        if (st == 1 && key) {
+            const Two lse = sm.lse[k], d = two_sum(unord32((unsigned)(key >> 32)), -lse.hi);
+            x = ord_two(add(Two{sm.cum[k], 0.f}, Two{d.hi, d.lo - lse.lo}));
+            where = ((unsigned long long)k << 32) | ~(unsigned)key;
+        } else if (st == 2 && i == k * per_row) {
+            x = ord_two(Two{sm.cum[k], 0.f});
+            where = ((unsigned long long)k << 32) | (unsigned)a.pad_token;
+        }
+        score[i] = x;
+        at[i] = where;
+        mine = x > mine ? x : mine;
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-        Cand y;
-        y.score = __shfl_xor_sync(0xffffffffu, mine.score, o);
-        y.at = __shfl_xor_sync(0xffffffffu, mine.at, o);
-        if (y.above(mine)) mine = y;
+        const unsigned long long y = __shfl_xor_sync(0xffffffffu, mine, o);
+        mine = y > mine ? y : mine;
     }
-    if (!mine.score) mine.at = (unsigned long long)(kQuads - 1 - (tid >> 2));  // none, but different in every quad
     if ((lane & 3) == 0) sm.top[tid >> 2] = mine;
     __syncthreads();
     if (tid < kQuads) {
-        const Cand x = sm.top[tid];
-        int r = 0;
+        const unsigned long long x = sm.top[tid];
+        const ulonglong2* t2 = reinterpret_cast<const ulonglong2*>(sm.top);
+        int above = 0, level = 0;
 #pragma unroll 8
-        for (int i = 0; i < kQuads; ++i) r += sm.top[i].above(x);
-        if (r == M - 1) sm.threshold = x;
+        for (int i = 0; i < kQuads / 2; ++i) {
+            const ulonglong2 t = t2[i];
+            above += (t.x > x) + (t.y > x);
+            level += (t.x == x) + (t.y == x);
+        }
+        if (above < M && above + level >= M) sm.threshold = x;  // equal scores write the same
     }
     __syncthreads();
-    const Cand thr = sm.threshold;
-    if (mine.score && !thr.above(mine)) {
+    const unsigned long long thr = sm.threshold;
+    if (mine && mine >= thr) {
         for (int i = tid; i < total; i += kThreads) {
-            const Cand x = cands[i];
-            if (x.score && !thr.above(x)) list[atomicAdd(&sm.found, 1)] = i;
+            const unsigned long long x = score[i];
+            if (x && x >= thr) {
+                const int to = atomicAdd(&sm.found, 1);
+                list_score[to] = x;
+                list_at[to] = at[i];
+            }
         }
     }
     __syncthreads();
 
-    // ---- 3. ranked by counting
+    // ---- 3. ranked by counting; equal scores by beam and token
     const int found = sm.found;
     for (int i = tid; i < found; i += kThreads) {
-        const Cand x = cands[list[i]];
-        int q = 0;
+        const unsigned long long x = list_score[i], where = list_at[i];
+        const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(list_score);
+        int q = 0, level = 0;
 #pragma unroll 4
-        for (int j = 0; j < found; ++j) q += cands[list[j]].above(x);
+        for (int o = 0; o < found / 2; ++o) {
+            const ulonglong2 y = l2[o];
+            q += (y.x > x) + (y.y > x);
+            level += (y.x == x) + (y.y == x);
+        }
+        if (found & 1) {
+            q += list_score[found - 1] > x;
+            level += list_score[found - 1] == x;
+        }
+        if (q >= M) continue;
+        if (level > 1)
+            for (int o = 0; o < found; ++o) q += list_score[o] == x && list_at[o] < where;
         if (q < M) {
-            const unsigned long long at = ~x.at;
-            a.out_scores[(long long)n * M + q] = (float)unord64(x.score);
-            a.out_parents[(long long)n * M + q] = n * K + (int)(at >> 32);
-            a.out_tokens[(long long)n * M + q] = (int)(unsigned)at;
+            a.out_scores[(long long)n * M + q] = unord32((unsigned)(x >> 32));
+            a.out_parents[(long long)n * M + q] = n * K + (int)(where >> 32);
+            a.out_tokens[(long long)n * M + q] = (int)(unsigned)where;
         }
     }
     if (tid >= found && tid < M) {
