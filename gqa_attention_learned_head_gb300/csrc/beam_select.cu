@@ -216,15 +216,18 @@ __device__ __forceinline__ float warp_max(float v) {
     return v;
 }
 
-// How many of the n keys are above `key` (n a multiple of 2, the array 16-byte aligned).
-__device__ __forceinline__ int rank_of(const unsigned long long* keys, int n, unsigned long long key) {
-    int r = 0;
-    const ulonglong2* k2 = reinterpret_cast<const ulonglong2*>(keys);
-#pragma unroll 8
-    for (int i = 0; i < n / 2; ++i) {
-        const ulonglong2 k = k2[i];
-        r += (k.x > key) + (k.y > key);
+// How many of the n keys are above `key` (low half) and equal to it (high half), counted by LANES neighbouring
+// threads together; every thread of the warp calls it, `sub` is the thread's number among the LANES.
+template <int LANES>
+__device__ __forceinline__ unsigned rank_of(const unsigned long long* keys, int n, unsigned long long key, int sub) {
+    unsigned r = 0;
+#pragma unroll 4
+    for (int i = sub; i < n; i += LANES) {
+        const unsigned long long k = keys[i];
+        r += k > key ? 1u : (k == key ? 0x10000u : 0u);
     }
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     return r;
 }
 
@@ -235,14 +238,56 @@ struct Gather {
     int best_g;
 };
 
-// One pass over the share; every group's maximum goes to gmax.  A group is two neighbouring threads' units.
+// One unit's words: its group's maximum to gmax, its exponentials to the sums.
+template <int DT>
+__device__ __forceinline__ void take(const uint32_t* w, int u, bool store, float* gmax, Gather& t) {
+    float x[kUnit];
+    Elem<DT>::unpack(w, x);
+    float m4[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
+    float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
+    if (store) gmax[u >> 1] = gm;
+    t.best_g = gm > t.best ? u >> 1 : t.best_g;
+    t.best = fmaxf(t.best, gm);
+    // sums up to 2^kSlack times the reference's lose nothing, so it moves once or twice a row, not with every new
+    // maximum (in a warp, one thread or another meets one nearly every time)
+    if (gm * kL > t.r2 + kSlack) {
+        const float r = ceilf(gm * kL), f = pow2_down(t.r2 - r);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) t.s2[i] = make_float2(t.s2[i].x * f, t.s2[i].y * f);
+        t.r2 = r;
+    }
+    const float2 l2 = make_float2(kL, kL), neg = make_float2(-t.r2, -t.r2);
+#pragma unroll
+    for (int i = 0; i < kUnit / 2; ++i) {
+        const float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), l2, neg);
+        t.s2[i & 1] = fadd2(t.s2[i & 1], make_float2(fast_exp2(y.x), fast_exp2(y.y)));
+    }
+}
+
+// One pass over the share.  A group is two neighbouring threads' units.
 template <int DT, bool ALIGNED>
 __device__ __forceinline__ void stream(const Share<DT>& sh, float* gmax, Gather& t) {
     using E = Elem<DT>;
     constexpr int kWords = Share<DT>::kWords, kHeld = kWords + (ALIGNED ? 0 : 8);
     constexpr int kBatch = ALIGNED ? 32 / kWords : (kWords == 16 ? 1 : 2);  // units loaded together
     const int tid = threadIdx.x;
-    for (int u0 = tid; u0 - (tid & 31) < sh.units; u0 += kThreads * kBatch) {  // whole warps
+    int u0 = tid;
+    if constexpr (ALIGNED) {  // while every unit of the warp's step is whole: no tests
+        const char* c = reinterpret_cast<const char*>(sh.p) + (size_t)tid * (kWords * 4);
+        for (; (u0 | 31) + (kBatch - 1) * kThreads < sh.hi; u0 += kThreads * kBatch, c += kThreads * kBatch * (kWords * 4)) {
+            uint32_t w[kBatch][kWords];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int i = 0; i < kWords / 8; ++i) load_sector(c + b * kThreads * (kWords * 4) + 32 * i, &w[b][8 * i]);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) take<DT>(w[b], u0 + b * kThreads, !(tid & 1), gmax, t);
+        }
+    }
+    for (; u0 - (tid & 31) < sh.units; u0 += kThreads * kBatch) {  // whole warps
         uint32_t w[kBatch][kHeld];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
@@ -257,31 +302,8 @@ __device__ __forceinline__ void stream(const Share<DT>& sh, float* gmax, Gather&
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int u = u0 + b * kThreads;
-            float x[kUnit];
             if constexpr (!ALIGNED) sh.settle(u, w[b]);
-            E::unpack(w[b], x);
-            float m4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
-            float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
-            gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
-            if (!(tid & 1) && u < sh.units) gmax[u >> 1] = gm;
-            t.best_g = gm > t.best ? u >> 1 : t.best_g;
-            t.best = fmaxf(t.best, gm);
-            // sums up to 2^kSlack times the reference's lose nothing, so it moves once or twice a row, not with
-            // every new maximum (in a warp, one thread or another meets one nearly every time)
-            if (gm * kL > t.r2 + kSlack) {
-                const float r = ceilf(gm * kL), f = pow2_down(t.r2 - r);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) t.s2[i] = make_float2(t.s2[i].x * f, t.s2[i].y * f);
-                t.r2 = r;
-            }
-            const float2 l2 = make_float2(kL, kL), neg = make_float2(-t.r2, -t.r2);
-#pragma unroll
-            for (int i = 0; i < kUnit / 2; ++i) {
-                const float2 y = ffma2(make_float2(x[2 * i], x[2 * i + 1]), l2, neg);
-                t.s2[i & 1] = fadd2(t.s2[i & 1], make_float2(fast_exp2(y.x), fast_exp2(y.y)));
-            }
+            take<DT>(w[b], u, !(tid & 1) && u < sh.units, gmax, t);
         }
     }
 }
@@ -376,29 +398,14 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     }
 
     // ---- 3. the threshold: the M-th best of the quads' best groups; meanwhile the last warp adds the sums up
-    if (tid < kQuads) {
-        const unsigned long long key = sm.top[tid];
-        if (rank_of(sm.top, kQuads, key) == M - 1) sm.threshold = key;
-    } else if (warp == kThreads / 32 - 1) {
-        float r = kNegInf;
+    if ((rank_of<4>(sm.top, kQuads, top, lane & 3) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = top;  // a quad's four
+    // the last warp adds the threads' sums up meanwhile, a part of it in each of the next stages
+    const bool adds = warp == kThreads / 32 - 1;
+    float r_all = kNegInf;
+    if (adds) {
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) r = fmaxf(r, sm.r[lane + 32 * i]);
-        r = warp_max(r);
-        Two sum = {0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {  // scaled by exact powers of two (a NaN stays one)
-            const float x = far ? sm.s[lane + 32 * i] : sm.s[lane + 32 * i] * pow2_down(sm.r[lane + 32 * i] - r);
-            sum = add(sum, Two{x, 0.f});
-        }
-        sum = warp_sum(sum, 32);
-        if (lane == 0) {
-            BeamPart out;
-            out.r2 = far ? kInf : r;
-            out.m = m_all;
-            out.hi = sum.hi;
-            out.lo = sum.lo;
-            a.part[blockIdx.x] = out;
-        }
+        for (int i = 0; i < kThreads / 32; ++i) r_all = fmaxf(r_all, sm.r[lane + 32 * i]);
+        r_all = warp_max(r_all);
     }
     __syncthreads();
     const unsigned long long thr = sm.threshold;
@@ -416,13 +423,25 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
             }
         }
     }
+    Two sum = {0.f, 0.f};
+    if (adds) {
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {  // scaled by exact powers of two (a NaN stays one)
+            const float x = far ? sm.s[lane + 32 * i] : sm.s[lane + 32 * i] * pow2_down(sm.r[lane + 32 * i] - r_all);
+            sum = add(sum, Two{x, 0.f});
+        }
+    }
     __syncthreads();
     const int n = sm.found[0];  // <= M x (groups of a quad)
-    for (int i = tid; i < n; i += kThreads) {
-        const unsigned long long key = list[i];
-        int r = rank_of(list, n & ~1, key);
-        if (n & 1) r += list[n - 1] > key;
-        if (r < M) sm.sel[r] = (int)~(unsigned)key;
+    for (int i0 = 0; i0 < n; i0 += kThreads / 8) {
+        const int i = i0 + (tid >> 3);
+        const unsigned long long key = i < n ? list[i] : 0ull;
+        const int r = (int)(rank_of<8>(list, n, key, lane & 7) & 0xffffu);
+        if (i < n && r < M) sm.sel[r] = (int)~(unsigned)key;
+    }
+    if (adds) {
+        sum = warp_sum(sum, 32);
+        if (lane == 0) a.part[blockIdx.x] = BeamPart{far ? kInf : r_all, m_all, sum.hi, sum.lo};
     }
     __syncthreads();
 
@@ -439,11 +458,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     __syncthreads();
     const int nt = sm.found[1];
     unsigned long long* out = a.best + (size_t)blockIdx.x * M;
-    for (int i = tid; i < nt; i += kThreads) {
-        const unsigned long long key = tokens[i];
-        int r = rank_of(tokens, nt & ~1, key);
-        if (nt & 1) r += tokens[nt - 1] > key;
-        if (r < M) out[r] = key;
+    for (int i0 = 0; i0 < nt; i0 += kThreads / 8) {
+        const int i = i0 + (tid >> 3);
+        const unsigned long long key = i < nt ? tokens[i] : 0ull;
+        const int r = (int)(rank_of<8>(tokens, nt, key, lane & 7) & 0xffffu);
+        if (i < nt && r < M && (lane & 7) == 0) out[r] = key;
     }
     if (tid >= nt && tid < M) out[tid] = 0;
 }
@@ -610,17 +629,9 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     }
     if ((lane & 3) == 0) sm.top[tid >> 2] = mine;
     __syncthreads();
-    if (tid < kQuads) {
-        const unsigned long long x = sm.top[tid];
-        const ulonglong2* t2 = reinterpret_cast<const ulonglong2*>(sm.top);
-        int above = 0, level = 0;
-#pragma unroll 8
-        for (int i = 0; i < kQuads / 2; ++i) {
-            const ulonglong2 t = t2[i];
-            above += (t.x > x) + (t.y > x);
-            level += (t.x == x) + (t.y == x);
-        }
-        if (above < M && above + level >= M) sm.threshold = x;  // equal scores write the same
+    {
+        const unsigned r = rank_of<4>(sm.top, kQuads, mine, lane & 3), above = r & 0xffffu, level = r >> 16;
+        if (above < (unsigned)M && above + level >= (unsigned)M) sm.threshold = mine;  // equal scores write the same
     }
     __syncthreads();
     const unsigned long long thr = sm.threshold;
@@ -638,23 +649,16 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
 
     // ---- 3. ranked by counting; equal scores by beam and token
     const int found = sm.found;
-    for (int i = tid; i < found; i += kThreads) {
-        const unsigned long long x = list_score[i], where = list_at[i];
-        const ulonglong2* l2 = reinterpret_cast<const ulonglong2*>(list_score);
-        int q = 0, level = 0;
+    for (int i0 = 0; i0 < found; i0 += kThreads / 8) {
+        const int i = i0 + (tid >> 3);
+        const unsigned long long x = i < found ? list_score[i] : 0ull, where = i < found ? list_at[i] : 0ull;
+        int q = 0;
 #pragma unroll 4
-        for (int o = 0; o < found / 2; ++o) {
-            const ulonglong2 y = l2[o];
-            q += (y.x > x) + (y.y > x);
-            level += (y.x == x) + (y.y == x);
-        }
-        if (found & 1) {
-            q += list_score[found - 1] > x;
-            level += list_score[found - 1] == x;
-        }
-        if (q >= M) continue;
-        if (level > 1)
-            for (int o = 0; o < found; ++o) q += list_score[o] == x && list_at[o] < where;
+        for (int o = lane & 7; o < found; o += 8)
+            q += (list_score[o] > x) | ((list_score[o] == x) & (list_at[o] < where));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+        if (i >= found || (lane & 7) != 0) continue;
         if (q < M) {
             a.out_scores[(long long)n * M + q] = unord32((unsigned)(x >> 32));
             a.out_parents[(long long)n * M + q] = n * K + (int)(where >> 32);
@@ -694,7 +698,7 @@ cudaError_t beam_plan(int N, int K, int V, int M, BeamPlan* plan) {
     const long long fine = V / 4096;
     if (parts > fine) parts = fine;
     const long long least = (V + kBeamMaxPart - 1) / kBeamMaxPart;
-    if (parts > kBeamMaxCands / 2 / ((long long)K * M)) parts = kBeamMaxCands / 2 / ((long long)K * M);
+    if (parts > kBeamMaxCands / 8 / ((long long)K * M)) parts = kBeamMaxCands / 8 / ((long long)K * M);
     if (parts < least) parts = least;
     if (parts < 1) parts = 1;
     const long long len = ((V + parts - 1) / parts + kGroup - 1) / kGroup * kGroup;
