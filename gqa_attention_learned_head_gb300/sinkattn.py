@@ -57,6 +57,11 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _raw_stream(device):
+    """The current stream of device number ``device``, as an integer."""
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
 def _need(t, name, dtype, ndim):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -342,16 +347,10 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
 
 
 # ---- a beam step over the paged cache -------------------------------------------------------------
+# These calls are short on the GPU, so their host path is kept short: plain integers instead of pointer objects, and
+# the raw handle of the current stream.
 
 _LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-
-
-def _here(*tensors):
-    """The tensors lie on the current device (the one the call's stream belongs to)."""
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != current:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
 
 
 def _on_stream(fn):
@@ -366,23 +365,39 @@ def _on_stream(fn):
     return call
 
 
-def _workspace(workspace, nbytes, device, what):
-    if workspace is not None:
-        return workspace
-    if nbytes == 0:
-        raise SinkAttnError(ERR_INVALID_ARG, what)
-    return torch.empty(nbytes, device=device, dtype=torch.uint8)
+def _here(*tensors):
+    """The index of the current device, on which all the tensors lie (the one the call's stream belongs to)."""
+    current = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != current:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
+    return current
 
 
-def _out(t, name, dtype, shape, device):
+def _at(t):
+    """A tensor's address for a void pointer argument."""
+    return None if t is None else t.data_ptr()
+
+
+def _out(t, name, dtype, shape, like):
     """An output: the given tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, device=device, dtype=dtype)
+        return torch.empty(shape, device=like.device, dtype=dtype)
     _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     _here(t)
     return t
+
+
+def _room(workspace, nbytes, like):
+    """(workspace, its bytes): the caller's, or a new one of ``nbytes``."""
+    if workspace is None:
+        return torch.empty(nbytes, device=like.device, dtype=torch.uint8), nbytes
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    _here(workspace)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def beam_dims(logits, num_select, pad_token=0) -> BeamDims:
@@ -411,30 +426,33 @@ def sinkattn_beam_select(logits, scores, num_select, finished=None, pad_token=0,
     if logits.dim() != 3 or logits.shape[1] == 0 or logits.shape[2] == 0:
         raise ValueError(f"logits must be [N, K, V], got shape {tuple(logits.shape)}")
     N, K, V = logits.shape
-    if (V > 1 and logits.stride(2) != 1) or (N > 1 and K > 1 and logits.stride(0) != K * logits.stride(1)):
+    if not logits.is_contiguous() and ((V > 1 and logits.stride(2) != 1) or
+                                       (N > 1 and K > 1 and logits.stride(0) != K * logits.stride(1))):
         raise ValueError("logits must have contiguous tokens and rows at one distance from each other")
     _need(scores, "scores", torch.float32, 2)
-    if tuple(scores.shape) != (N, K):
+    if scores.shape != (N, K):
         raise ValueError("scores must be [N, K]")
     if finished is not None:
         _need(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, 2)
-        if tuple(finished.shape) != (N, K):
+        if finished.shape != (N, K):
             raise ValueError("finished must be [N, K]")
-    _here(logits, scores, finished)
+    device = _here(logits, scores, finished)
     M = int(num_select)
     dims = beam_dims(logits, M, int(pad_token))
-    nbytes = int(_lib.sinkattn_beam_select_workspace_size(ctypes.byref(dims)))
-    if nbytes == 0:
-        st = _lib.sinkattn_beam_select(None, None, None, None, None, None, ctypes.byref(dims), None, 0, None)
+    ref = ctypes.byref(dims)
+    nbytes = _lib.sinkattn_beam_select_workspace_size(ref)
+    if nbytes == 0:  # invalid dims: the call says why
+        st = _lib.sinkattn_beam_select(None, None, None, None, None, None, ref, None, 0, None)
         raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_beam_select")
-    out_scores = _out(out_scores, "out_scores", torch.float32, (N, M), logits.device)
-    out_parents = _out(out_parents, "out_parents", torch.int32, (N, M), logits.device)
-    out_tokens = _out(out_tokens, "out_tokens", torch.int32, (N, M), logits.device)
-    workspace = _workspace(workspace, nbytes, logits.device, "sinkattn_beam_select_workspace_size")
-    st = _lib.sinkattn_beam_select(_ptr(logits), _ptr(scores), _ptr(finished), _ptr(out_scores), _ptr(out_parents),
-                                   _ptr(out_tokens), ctypes.byref(dims), _ptr(workspace),
-                                   workspace.numel() * workspace.element_size(), _stream(None))
-    _check(st, "sinkattn_beam_select")
+    out_scores = _out(out_scores, "out_scores", torch.float32, (N, M), logits)
+    out_parents = _out(out_parents, "out_parents", torch.int32, (N, M), logits)
+    out_tokens = _out(out_tokens, "out_tokens", torch.int32, (N, M), logits)
+    workspace, nbytes = _room(workspace, nbytes, logits)
+    st = _lib.sinkattn_beam_select(logits.data_ptr(), scores.data_ptr(), _at(finished), out_scores.data_ptr(),
+                                   out_parents.data_ptr(), out_tokens.data_ptr(), ref, workspace.data_ptr(), nbytes,
+                                   _raw_stream(device))
+    if st != OK:
+        raise SinkAttnError(st, "sinkattn_beam_select")
     return out_scores, out_parents, out_tokens
 
 
@@ -452,7 +470,8 @@ def sinkattn_pages_fork(page_table, held_lens, parents, page_refs, keep_lens=Non
     _need(held_lens, "held_lens", torch.int32, 1)
     _need(parents, "parents", torch.int32, 1)
     _need(page_refs, "page_refs", torch.int32, 1)
-    R, Rin, mp, P = parents.shape[0], page_table.shape[0], page_table.shape[1], page_refs.shape[0]
+    Rin, mp = page_table.shape
+    R, P = parents.shape[0], page_refs.shape[0]
     if held_lens.shape[0] != Rin:
         raise ValueError("held_lens must have one entry per row of page_table")
     for t, name in ((keep_lens, "keep_lens"), (room_lens, "room_lens")):
@@ -460,21 +479,24 @@ def sinkattn_pages_fork(page_table, held_lens, parents, page_refs, keep_lens=Non
             _need(t, name, torch.int32, 1)
             if t.shape[0] != R:
                 raise ValueError(f"{name} must have one entry per new row")
-    _here(page_table, held_lens, parents, page_refs, keep_lens, room_lens)
-    dev = page_table.device
-    out_table = _out(out_table, "out_table", torch.int32, (R, mp), dev)
-    out_lens = _out(out_lens, "out_lens", torch.int32, (R,), dev)
-    out_refs = _out(out_refs, "out_refs", torch.int32, (P,), dev)
-    copies = _out(copies, "copies", torch.int32, (R, 3), dev)
+    device = _here(page_table, held_lens, parents, page_refs, keep_lens, room_lens)
     dims = ForkDims(Rin, R, P, mp, 16, int(grow))
-    if workspace is None:
-        workspace = _workspace(None, int(_lib.sinkattn_pages_fork_workspace_size(ctypes.byref(dims))), dev,
-                               "sinkattn_pages_fork_workspace_size")
-    st = _lib.sinkattn_pages_fork(_ptr(page_table), _ptr(held_lens), _ptr(parents), _ptr(keep_lens), _ptr(room_lens),
-                                  _ptr(page_refs), _ptr(out_table), _ptr(out_lens), _ptr(out_refs), _ptr(copies),
-                                  ctypes.byref(dims), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  _stream(None))
-    _check(st, "sinkattn_pages_fork")
+    ref = ctypes.byref(dims)
+    nbytes = _lib.sinkattn_pages_fork_workspace_size(ref)
+    if nbytes == 0:  # invalid dims: the call says why
+        st = _lib.sinkattn_pages_fork(*[None] * 10, ref, None, 0, None)
+        raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_pages_fork")
+    out_table = _out(out_table, "out_table", torch.int32, (R, mp), page_table)
+    out_lens = _out(out_lens, "out_lens", torch.int32, (R,), page_table)
+    out_refs = _out(out_refs, "out_refs", torch.int32, (P,), page_table)
+    copies = _out(copies, "copies", torch.int32, (R, 3), page_table)
+    workspace, nbytes = _room(workspace, nbytes, page_table)
+    st = _lib.sinkattn_pages_fork(page_table.data_ptr(), held_lens.data_ptr(), parents.data_ptr(), _at(keep_lens),
+                                  _at(room_lens), page_refs.data_ptr(), out_table.data_ptr(), out_lens.data_ptr(),
+                                  out_refs.data_ptr(), copies.data_ptr(), ref, workspace.data_ptr(), nbytes,
+                                  _raw_stream(device))
+    if st != OK:
+        raise SinkAttnError(st, "sinkattn_pages_fork")
     return out_table, out_lens, out_refs, copies
 
 
@@ -495,10 +517,12 @@ def sinkattn_kv_copy(k_pages, v_pages, copies):
     _need(copies, "copies", torch.int32, 2)
     if copies.shape[1] != 3:
         raise ValueError("copies must be [n, 3]")
-    _here(k_pages, v_pages, copies)
+    device = _here(k_pages, v_pages, copies)
     dims = MoveDims(L, copies.shape[0], Hkv, D, PS, P, 0, 0)
-    _check(_lib.sinkattn_kv_copy(_ptr(k_pages), _ptr(v_pages), _ptr(copies), ctypes.byref(dims), _stream(None)),
-           "sinkattn_kv_copy")
+    st = _lib.sinkattn_kv_copy(k_pages.data_ptr(), v_pages.data_ptr(), copies.data_ptr(), ctypes.byref(dims),
+                               _raw_stream(device))
+    if st != OK:
+        raise SinkAttnError(st, "sinkattn_kv_copy")
 
 
 @_on_stream
@@ -510,13 +534,15 @@ def sinkattn_kv_compact(k_pages, v_pages, page_table, start_pos, accepted, num_a
     _need(start_pos, "start_pos", torch.int32, 1)
     _need(accepted, "accepted", torch.int32, 2)
     _need(num_accepted, "num_accepted", torch.int32, 1)
-    B = accepted.shape[0]
+    B, A = accepted.shape
     if page_table.shape[0] != B or start_pos.shape[0] != B or num_accepted.shape[0] != B:
         raise ValueError("inconsistent compact shapes")
-    _here(k_pages, v_pages, page_table, start_pos, accepted, num_accepted)
-    dims = MoveDims(L, B, Hkv, D, PS, P, page_table.shape[1], accepted.shape[1])
-    _check(_lib.sinkattn_kv_compact(_ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(start_pos), _ptr(accepted),
-                                    _ptr(num_accepted), ctypes.byref(dims), _stream(None)), "sinkattn_kv_compact")
+    device = _here(k_pages, v_pages, page_table, start_pos, accepted, num_accepted)
+    dims = MoveDims(L, B, Hkv, D, PS, P, page_table.shape[1], A)
+    st = _lib.sinkattn_kv_compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), start_pos.data_ptr(),
+                                  accepted.data_ptr(), num_accepted.data_ptr(), ctypes.byref(dims), _raw_stream(device))
+    if st != OK:
+        raise SinkAttnError(st, "sinkattn_kv_compact")
 
 
 def beams_dims(q, k_pages, page_table, num_workers=0) -> BeamsDims:
@@ -545,24 +571,24 @@ def sinkattn_decode_beams(q, k_pages, v_pages, page_table, kv_lens, sinks, scale
     if v_pages.shape != k_pages.shape:
         raise ValueError("k_pages and v_pages must have the same shape")
     N, K, Hq, D = q.shape
-    if tuple(page_table.shape[:2]) != (N, K) or tuple(kv_lens.shape) != (N, K) or sinks.shape[0] != Hq:
+    if page_table.shape[:2] != (N, K) or kv_lens.shape != (N, K) or sinks.shape[0] != Hq:
         raise ValueError("inconsistent decode_beams shapes")
-    _here(q, k_pages, v_pages, page_table, kv_lens, sinks)
+    device = _here(q, k_pages, v_pages, page_table, kv_lens, sinks)
     dims = beams_dims(q, k_pages, page_table, num_workers)
-    out = _out(out, "out", torch.bfloat16, tuple(q.shape), q.device)
+    ref = ctypes.byref(dims)
+    nbytes = _lib.sinkattn_decode_beams_workspace_size(ref)
+    if nbytes == 0:  # invalid dims: the call says why
+        st = _lib.sinkattn_decode_beams(None, None, None, None, None, None, float(scale), None, None, ref, None, 0, None)
+        raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_decode_beams")
+    out = _out(out, "out", torch.bfloat16, (N, K, Hq, D), q)
     if lse is not None or return_lse:
-        lse = _out(lse, "lse", torch.float32, (N, K, Hq), q.device)
-    if workspace is None:
-        nbytes = int(_lib.sinkattn_decode_beams_workspace_size(ctypes.byref(dims)))
-        if nbytes == 0:
-            st = _lib.sinkattn_decode_beams(None, None, None, None, None, None, float(scale), None, None,
-                                            ctypes.byref(dims), None, 0, None)
-            raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_decode_beams")
-        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
-    st = _lib.sinkattn_decode_beams(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(sinks),
-                                    float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream(None))
-    _check(st, "sinkattn_decode_beams")
+        lse = _out(lse, "lse", torch.float32, (N, K, Hq), q)
+    workspace, nbytes = _room(workspace, nbytes, q)
+    st = _lib.sinkattn_decode_beams(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+                                    kv_lens.data_ptr(), sinks.data_ptr(), float(scale), out.data_ptr(), _at(lse), ref,
+                                    workspace.data_ptr(), nbytes, _raw_stream(device))
+    if st != OK:
+        raise SinkAttnError(st, "sinkattn_decode_beams")
     return out, lse
 
 
