@@ -35,7 +35,8 @@ sinkattn_status_t check_fork_dims(const sinkattn_fork_dims_t* d) {
     if (!d) return SINKATTN_ERR_INVALID_ARG;
     if (d->num_rows_in < 0 || d->num_rows_out < 0 || d->num_pages < 0 || d->max_pages < 1 || d->grow < 0)
         return SINKATTN_ERR_INVALID_ARG;
-    if (d->page_size != kPageSize || d->num_rows_in > (1 << 20) || d->num_rows_out > (1 << 20))
+    if (d->page_size != kPageSize || d->num_rows_in > (1 << 20) || d->num_rows_out > (1 << 20) ||
+        d->num_pages > (1 << 30))
         return SINKATTN_ERR_UNSUPPORTED;
     if ((long long)d->max_pages * kPageSize >= (1ll << 31)) return SINKATTN_ERR_UNSUPPORTED;
     return SINKATTN_OK;
@@ -129,7 +130,9 @@ sinkattn_status_t sinkattn_beam_select(const void* logits, const float* scores, 
 
 size_t sinkattn_pages_fork_workspace_size(const sinkattn_fork_dims_t* dims) {
     if (check_fork_dims(dims) != SINKATTN_OK) return 0;
-    return fork_workspace(dims->num_rows_in, dims->num_rows_out, dims->num_pages);
+    ForkPlan plan;
+    fork_plan(dims->num_rows_in, dims->num_rows_out, dims->num_pages, &plan);
+    return plan.ws_bytes;
 }
 
 sinkattn_status_t sinkattn_pages_fork(const int32_t* page_table, const int32_t* held_lens, const int32_t* parents,
@@ -157,9 +160,9 @@ sinkattn_status_t sinkattn_pages_fork(const int32_t* page_table, const int32_t* 
     }
     DeviceState* ds = nullptr;
     if ((st = device_state(&ds)) != SINKATTN_OK) return st;
-    if (!workspace || workspace_bytes < fork_workspace(d.num_rows_in, d.num_rows_out, d.num_pages) ||
-        !aligned(workspace, 256))
-        return SINKATTN_ERR_WORKSPACE;
+    ForkPlan plan;
+    fork_plan(d.num_rows_in, d.num_rows_out, d.num_pages, &plan);
+    if (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)) return SINKATTN_ERR_WORKSPACE;
     ForkArgs a;
     a.page_table = page_table;
     a.held_lens = held_lens;
@@ -171,13 +174,14 @@ sinkattn_status_t sinkattn_pages_fork(const int32_t* page_table, const int32_t* 
     a.out_lens = out_lens;
     a.refs_out = out_refs;
     a.copies = copies;
-    int32_t* ws = static_cast<int32_t*>(workspace);
-    a.ok = ws;
-    a.first = ws + 1;
-    a.low = a.first + d.num_rows_in;
-    a.high = a.low + d.num_rows_in;
-    a.at = a.high + d.num_rows_in;
-    a.free_ids = a.at + d.num_rows_out;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.rows = reinterpret_cast<int4*>(ws);
+    a.drops = reinterpret_cast<int2*>(ws + plan.drops);
+    a.first = reinterpret_cast<int32_t*>(ws + plan.first);
+    a.low = reinterpret_cast<int32_t*>(ws + plan.low);
+    a.high = reinterpret_cast<int32_t*>(ws + plan.high);
+    a.free_ids = reinterpret_cast<int32_t*>(ws + plan.free_ids);
+    a.ok = reinterpret_cast<int32_t*>(ws + plan.ok);
     a.err = ds->err;
     a.Rin = d.num_rows_in;
     a.Rout = d.num_rows_out;

@@ -18,17 +18,21 @@ struct ForkArgs {
     int32_t* refs_out;          // [P], may be refs_in
     int32_t* copies;            // [Rout, 3]
     // workspace
+    int4* rows;                 // [Rout] parent, keep, room (top bit: the parent's first child), where its new pages
+                                //        start in free_ids (top bit: the first replaces its last kept page)
+    int2* drops;                // [Rin] the columns that this row holds and its first child does not keep
     int32_t* first;             // [Rin] lowest row that continues this one, INT_MAX: none
     int32_t* low;               // [Rin] least and greatest keep of the rows that continue this one and will
     int32_t* high;              //       write their last page (-1 for one that will not)
-    int32_t* at;                // [Rout] where this row's new pages start in free_ids; top bit: the first of
-                                //        them replaces its last kept page
     int32_t* free_ids;          // [P] free pages, lowest first (as many as are needed)
     int32_t* ok;                // [1] 1: there are enough of them
     unsigned* err;
     int Rin, Rout, P, max_pages, grow;
 };
-size_t fork_workspace(int Rin, int Rout, int P);
+struct ForkPlan {
+    size_t drops, first, low, high, free_ids, ok, ws_bytes;  // offsets in the workspace (rows at 0)
+};
+void fork_plan(int Rin, int Rout, int P, ForkPlan* plan);
 cudaError_t pages_fork_launch(const ForkArgs& args, cudaStream_t stream);
 
 // ------------------------------------------------------------------ moves of cached tokens

@@ -3,17 +3,21 @@
 //
 // Whole numbers only.  With kc = ceil(keep / 16), rc = ceil(room / 16), hc = ceil(held / 16) columns, row r
 // takes columns [0, kc) from its parent, and rc - kc new pages (one more where its last kept page is replaced,
-// see row_of below).  The pages' counts change by
+// see replaces below).  The pages' counts change by
 //   +1 for every kept column of every child but a parent's first,
 //   -1 for every column that a parent holds beyond those its first child keeps (all of them without a child),
 // which is the sum over all rows with the first child's and its parent's +1 and -1 left out: a row that simply
 // goes on touches no count.  New pages count 1.  Additions commute, so no order shows in the result.
 //
 // fork_plan_kernel: one cluster of CTAs.  First, least and greatest keep of every parent's children (atomic
-// minimum and maximum), a prefix sum over the rows' needs and, in the same pass as the copy of the counts, the
-// lowest free pages, both by cluster-wide scans through distributed shared memory.  Its time is latency (three
-// cluster barriers around passes over a few MB in L2).  fork_apply_kernel: one CTA per row (new rows write
-// their table, present rows give up their columns), bound by the table's bytes and the counts' atomics.
+// minimum and maximum), a prefix sum over the rows' needs, and the lowest free pages from one pass over the counts
+// (which also copies them): a bit for every page of the pass stays in registers until the sums of the cluster
+// (through distributed shared memory) have said where each thread's free pages go.  Its time is latency: chains of
+// loads (a row's parent, its parent's tokens, its last page, that page's count) and barriers.  So up to kLocalRows
+// rows every CTA goes over all of them by itself, in shared memory, and the cluster meets once.
+// fork_apply_kernel: a thread takes one column of kBatch present and kBatch new rows, reads and writes their
+// entries, and adds up the changes to a page's count as long as neighbouring rows hold the same page: for the pages
+// that a group's rows share, drops and forks mostly cancel and no atomic is left.  Bound by the table's bytes.
 #include "args_pages.h"
 #include "ptx.cuh"
 
@@ -26,55 +30,71 @@ namespace sinkattn {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPass = 32 * kPlanThreads;  // pages that a CTA takes in one pass, a word of 32 a thread
+constexpr int kWords = 2;                 // passes whose words a thread keeps
+constexpr int kLocalRows = 4096;          // rows that every CTA of the plan goes over itself
 constexpr int kApplyThreads = 128;
+constexpr int kBatch = 8;                 // rows of a thread of the apply kernel
+constexpr unsigned kTop = 0x80000000u;
 
 __device__ __forceinline__ int cols(int tokens) { return (tokens + kPageSize - 1) / kPageSize; }
 
-// A present row's held tokens, clamped.
-__device__ __forceinline__ int held_of(const ForkArgs& a, int p) {
-    const int h = __ldcg(&a.held_lens[p]), cap = a.max_pages * kPageSize;
-    return h < 0 ? 0 : (h > cap ? cap : h);
-}
-
-// A new row's parent, kept and room tokens, brought into range; `bad` collects the error bits.
+// A new row's parent, kept and room tokens, brought into range, and the count of the page that it is going to
+// write: kNoPage if it writes none, or one that is not of the pool.
+constexpr int kNoPage = INT_MIN;
 struct Row {
-    int parent, keep, room;
-    bool writes;  // its last kept page is partial and will be written
+    int parent, keep, room, count;
+    __device__ bool writes() const { return room > keep && keep % kPageSize != 0; }  // its last kept page
 };
-__device__ __forceinline__ Row row_of(const ForkArgs& a, int r, unsigned& bad) {
+// Rows r .. r + n - 1 (n <= N), the loads of each kind issued together; `bad` collects the error bits.
+template <int N>
+__device__ __forceinline__ void load_rows(const ForkArgs& a, int r, int n, Row (&x)[N], unsigned& bad) {
     const int cap = a.max_pages * kPageSize;
-    Row x;
-    x.parent = __ldcg(&a.parents[r]);
-    if (x.parent < -1 || x.parent >= a.Rin) {
-        bad |= kErrBadIndex;
-        x.parent = -1;
-    }
-    const int held = x.parent >= 0 ? held_of(a, x.parent) : 0;
-    x.keep = held;
-    if (a.keep_lens) {
-        x.keep = __ldcg(&a.keep_lens[r]);
-        if (x.keep < 0 || x.keep > held) {
-            bad |= kErrBadLength;
-            x.keep = x.keep < 0 ? 0 : held;
+    int keep[N], room[N], held[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] = Row{-1, 0, 0, kNoPage};
+        keep[i] = room[i] = 0;
+        if (i < n) {
+            x[i].parent = __ldcg(&a.parents[r + i]);
+            if (a.keep_lens) keep[i] = __ldcg(&a.keep_lens[r + i]);
+            if (a.room_lens) room[i] = __ldcg(&a.room_lens[r + i]);
         }
     }
-    long long room = x.parent >= 0 ? (long long)x.keep + a.grow : 0;
-    if (a.room_lens) room = __ldcg(&a.room_lens[r]);
-    if (room < x.keep || room > cap) {
-        bad |= kErrBadLength;
-        room = room < x.keep ? x.keep : cap;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (x[i].parent < -1 || x[i].parent >= a.Rin) {
+            bad |= kErrBadIndex;
+            x[i].parent = -1;
+        }
+        held[i] = x[i].parent >= 0 ? __ldcg(&a.held_lens[x[i].parent]) : 0;
     }
-    x.room = (int)room;
-    x.writes = x.room > x.keep && x.keep % kPageSize != 0;
-    return x;
+    int page[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int h = held[i] < 0 ? 0 : (held[i] > cap ? cap : held[i]);  // reported where the parent is looked at
+        x[i].keep = h;
+        if (a.keep_lens) {
+            if (keep[i] < 0 || keep[i] > h) bad |= kErrBadLength;
+            x[i].keep = keep[i] < 0 ? 0 : (keep[i] > h ? h : keep[i]);
+        }
+        long long m = x[i].parent >= 0 ? (long long)x[i].keep + a.grow : 0;
+        if (a.room_lens) m = room[i];
+        if (m < x[i].keep || m > cap) {
+            if (i < n) bad |= kErrBadLength;
+            m = m < x[i].keep ? x[i].keep : cap;
+        }
+        x[i].room = i < n ? (int)m : 0;
+        page[i] = x[i].writes() ? __ldcg(&a.page_table[(long long)x[i].parent * a.max_pages + x[i].keep / kPageSize]) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (page[i] >= 0 && page[i] < a.P) x[i].count = __ldcg(&a.refs_in[page[i]]);
 }
-
-// Whether row r gets a new page in place of its last kept one.
-__device__ __forceinline__ bool replaces(const ForkArgs& a, int r, const Row& x, int first, int low, int high) {
-    if (!x.writes) return false;
-    const int page = __ldcg(&a.page_table[(long long)x.parent * a.max_pages + x.keep / kPageSize]);
-    if (page < 0 || page >= a.P) return false;  // not a page of the pool: carried along
-    return !(__ldcg(&a.refs_in[page]) == 1 && first == r && low == high);
+// Whether row r gets a new page in place of its last kept one: it will write that page (a page of the pool), and is
+// not the first of children that all keep the same and will write, of the page's one holder.
+__device__ __forceinline__ bool replaces(int r, int count, int first, int low, int high) {
+    return count != kNoPage && !(count == 1 && first == r && low == high);
 }
 
 // Inclusive prefix sum over the CTA's threads; `total` is the sum.  red: one word per warp.
@@ -88,7 +108,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
     __syncthreads();
     if (lane == 31) red[warp] = v;
     __syncthreads();
-    long long w = lane < kPlanThreads / 32 ? red[lane] : 0;
+    long long w = red[lane];
     const long long own = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -99,168 +119,396 @@ __device__ __forceinline__ long long block_scan(long long v, long long* red, lon
     return v + __shfl_sync(0xffffffffu, w - own, warp);
 }
 
+// Free pages among p .. p + 1023 (below `end`), p the warp's first: lane l's word has bit i set where page
+// p + 32 l + i is free.  Sixteen bytes a lane and step, eight steps in flight; a step's eight neighbouring lanes make a word.
+__device__ __forceinline__ unsigned free_word(const int* counts, bool wide, long long p, int end) {
+    const int lane = threadIdx.x & 31;
+    if (p >= end) return 0u;
+    int4 c[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const long long q = p + 128 * j + 4 * lane;
+        if (wide && q + 4 <= end) {
+            c[j] = __ldcg(reinterpret_cast<const int4*>(counts + q));
+        } else {
+            c[j].x = q < end ? __ldcg(counts + q) : -1;
+            c[j].y = q + 1 < end ? __ldcg(counts + q + 1) : -1;
+            c[j].z = q + 2 < end ? __ldcg(counts + q + 2) : -1;
+            c[j].w = q + 3 < end ? __ldcg(counts + q + 3) : -1;
+        }
+    }
+    unsigned mine = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        unsigned w = ((c[j].x == 0) | (c[j].y == 0) << 1 | (c[j].z == 0) << 2 | (c[j].w == 0) << 3) << (4 * (lane & 7));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+        mine = (lane & 7) == j ? w : mine;  // lane 8 g + j has word 4 j + g
+    }
+    return __shfl_sync(0xffffffffu, mine, 8 * (lane & 3) + (lane >> 2));
+}
+
+struct PlanSmem {
+    long long red[kPlanThreads / 32];
+    long long sums[2];  // this CTA's new pages needed, free pages found
+    int first[kLocalRows], low[kLocalRows], high[kLocalRows], keep[kLocalRows];  // LOCAL
+};
+
+// The first cluster plans, any further ones copy the counts.
+// LOCAL: every CTA of the cluster goes over all the rows, at most kLocalRows present and new ones, with the parents'
+// children in its own shared memory; else each over its part of the rows, with the children in the workspace.
+template <bool LOCAL>
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const ForkArgs a) {
-    __shared__ long long red[kPlanThreads / 32];
-    __shared__ long long sums[2];  // this CTA's new pages needed, free pages found
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    PlanSmem& sm = *reinterpret_cast<PlanSmem*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.refs_in) | reinterpret_cast<uintptr_t>(a.refs_out)) & 15) == 0;
+    if ((int)blockIdx.x >= ctas) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const long long first = (long long)((int)blockIdx.x - ctas) * kPlanThreads + tid;
+        const long long step = (long long)((int)gridDim.x - ctas) * kPlanThreads, quads = wide ? a.P / 4 : 0;
+        for (long long i = first; i < quads; i += step)
+            reinterpret_cast<int4*>(a.refs_out)[i] = __ldcg(reinterpret_cast<const int4*>(a.refs_in) + i);
+        for (long long i = 4 * quads + first; i < a.P; i += step) a.refs_out[i] = __ldcg(&a.refs_in[i]);
+        return;
+    }
+    int* first = LOCAL ? sm.first : a.first;
+    int* low = LOCAL ? sm.low : a.low;
+    int* high = LOCAL ? sm.high : a.high;
+    // the pages of this CTA, and the rows that it goes over, a run of `per` consecutive ones a thread; the last threads
+    // take the first rows, as the first take the first pages: with little to do, both run at once
+    const long long p_len = (((long long)a.P + ctas - 1) / ctas + 3) & ~3ll;
+    const int p0 = (int)min((long long)a.P, rank * p_len), p1 = (int)min((long long)a.P, p0 + p_len);
+    const int r_len = LOCAL ? a.Rout : (a.Rout + ctas - 1) / ctas, turned = kPlanThreads - 1 - tid;
+    const int r0 = LOCAL ? 0 : min(a.Rout, rank * r_len), r1 = min(a.Rout, r0 + r_len);
+    const int per = (r1 - r0 + kPlanThreads - 1) / kPlanThreads;
+    const int ra = (int)min((long long)r1, r0 + (long long)turned * per), rb = min(r1, ra + per);
+    const int stride = LOCAL ? kPlanThreads : kPlanThreads * ctas, start = LOCAL ? tid : rank * kPlanThreads + tid;
+    const bool report = !LOCAL || rank == 0;
+    unsigned bad = 0;
+    if constexpr (LOCAL)
+        for (int p = start; p < a.Rin; p += stride) {
+            first[p] = INT_MAX;
+            low[p] = INT_MAX;
+            high[p] = INT_MIN;
+        }
+    if (tid == 0) sm.sums[1] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
-    const int gt = rank * kPlanThreads + tid, gn = ctas * kPlanThreads;
-    unsigned bad = 0;
 
-    // ---- 1. each parent's children
-    for (int p = gt; p < a.Rin; p += gn) {
-        a.first[p] = INT_MAX;
-        a.low[p] = INT_MAX;
-        a.high[p] = INT_MIN;
-        const int h = __ldcg(&a.held_lens[p]);
-        if (h < 0 || h > a.max_pages * kPageSize) bad |= kErrBadLength;
+    // ---- 1. the rows (LOCAL: a thread's stay in registers), and the pass over the counts
+    constexpr int kHeld = LOCAL ? kLocalRows / kPlanThreads : 1;
+    Row held[kHeld];
+    if (ra < rb) load_rows(a, ra, min(kHeld, rb - ra), held, bad);
+    auto row = [&](int r, unsigned& seen) {
+        if constexpr (LOCAL) {
+            Row x = held[0];
+#pragma unroll
+            for (int i = 1; i < kHeld; ++i) x = r == ra + i ? held[i] : x;
+            return x;
+        } else {
+            if (r == ra) return held[0];
+            Row x[1];
+            load_rows(a, r, 1, x, seen);
+            return x[0];
+        }
+    };
+    if constexpr (!LOCAL)
+        for (int p = start; p < a.Rin; p += stride) {
+            first[p] = INT_MAX;
+            low[p] = INT_MAX;
+            high[p] = INT_MIN;
+        }
+    unsigned words[kWords];
+    int found = 0;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+        words[i] = free_word(a.refs_in, wide, (long long)p0 + (long long)i * kPass + 1024 * warp, p1);
+        found += __popc(words[i]);
     }
-    cluster.sync();
-    for (int r = gt; r < a.Rout; r += gn) {
-        const Row x = row_of(a, r, bad);
+    for (long long q = (long long)p0 + kWords * kPass; q < p1; q += kPass)  // read again below
+        found += __popc(free_word(a.refs_in, wide, q + 1024 * warp, p1));
+    found = __reduce_add_sync(0xffffffffu, found);
+    if constexpr (LOCAL) __syncthreads();
+    else cluster.sync();
+
+    // ---- 2. each parent's children
+    if (lane == 0 && found) atomicAdd(reinterpret_cast<unsigned long long*>(&sm.sums[1]), (unsigned long long)found);
+    for (int r = ra; r < rb; ++r) {
+        const Row x = row(r, bad);
+        if constexpr (LOCAL) sm.keep[r] = x.keep;
         if (x.parent < 0) continue;
-        const int mark = x.writes ? x.keep : -1;
-        atomicMin(&a.first[x.parent], r);
-        atomicMin(&a.low[x.parent], mark);
-        atomicMax(&a.high[x.parent], mark);
+        const int mark = x.writes() ? x.keep : -1;
+        atomicMin(&first[x.parent], r);
+        atomicMin(&low[x.parent], mark);
+        atomicMax(&high[x.parent], mark);
     }
-    if (bad) atomicOr(a.err, bad);
-    cluster.sync();
+    if constexpr (LOCAL) __syncthreads();
+    else cluster.sync();
 
-    // ---- 2. the rows' needs and the free pages, counted; each CTA a contiguous part of both
-    const int r_len = (a.Rout + ctas - 1) / ctas, r0 = min(a.Rout, rank * r_len), r1 = min(a.Rout, r0 + r_len);
-    const int p_len = ((a.P + ctas - 1) / ctas + 3) & ~3, p0 = min(a.P, rank * p_len), p1 = min(a.P, p0 + p_len);
-    auto need_of = [&](int r, bool& replace) {
+    // ---- 3. the rows' needs and their prefix; the sums of the cluster
+    auto need_of = [&](int r, Row& x, bool& replace, bool& is_first) {
         unsigned ignored = 0;
-        const Row x = row_of(a, r, ignored);
-        replace = x.parent >= 0 && replaces(a, r, x, __ldcg(&a.first[x.parent]), __ldcg(&a.low[x.parent]),
-                                            __ldcg(&a.high[x.parent]));
+        x = row(r, ignored);
+        replace = is_first = false;
+        if (x.parent >= 0) {
+            const int f = LOCAL ? first[x.parent] : __ldcg(&first[x.parent]);
+            const int lo = LOCAL ? low[x.parent] : __ldcg(&low[x.parent]), hi = LOCAL ? high[x.parent] : __ldcg(&high[x.parent]);
+            is_first = f == r;
+            replace = replaces(r, x.count, f, lo, hi);
+        }
         return cols(x.room) - cols(x.keep) + (int)replace;
     };
-    long long need = 0, free = 0, total;
-    bool replace = false;
-    for (int r = r0 + tid; r < r1; r += kPlanThreads) need += need_of(r, replace);
-    for (int p = p0 + tid; p < p1; p += kPlanThreads) {
-        const int c = __ldcg(&a.refs_in[p]);
-        free += c == 0;
-    }
-    block_scan(need, red, total);
-    if (tid == 0) sums[0] = total;
-    block_scan(free, red, total);
-    if (tid == 0) sums[1] = total;
+    Row x;
+    bool replace, is_first;
+    long long need = 0, need_all;
+    for (int r = ra; r < rb; ++r) need += need_of(r, x, replace, is_first);
+    // (the threads' prefix runs over the rows from behind)
+    long long at = block_scan(need, sm.red, need_all);
+    at = need_all - at;
+    if (tid == 0) sm.sums[0] = need_all;
     cluster.sync();
-    long long need_before = 0, need_all = 0, free_before = 0, free_all = 0;
+    long long free_before = 0, free_all = 0, need_sum = 0;
     for (int i = 0; i < ctas; ++i) {
-        const long long* s = cluster.map_shared_rank(sums, i);
-        need_before += i < rank ? s[0] : 0;
-        free_before += i < rank ? s[1] : 0;
-        need_all += s[0];
-        free_all += s[1];
+        const long long* s = cluster.map_shared_rank(sm.sums, i);
+        const long long n = s[0], f = s[1];
+        if (!LOCAL) at += i < rank ? n : 0;
+        free_before += i < rank ? f : 0;
+        need_sum += n;
+        free_all += f;
     }
-    cluster.sync();  // no CTA ends while another reads its sums
+    if (!LOCAL) need_all = need_sum;
+    auto leave = cluster.barrier_arrive();  // no CTA ends while another reads its sums
     const bool ok = need_all <= free_all;
     if (rank == 0 && tid == 0) {
         *a.ok = ok ? 1 : 0;
         if (!ok) atomicOr(a.err, kErrNoPages);
     }
 
-    // ---- 3. where each row's new pages start, and the lowest free pages in order; the counts are copied
-    for (int base = r0; base < r1; base += kPlanThreads) {
-        const int r = base + tid;
-        const int n = r < r1 ? need_of(r, replace) : 0;
-        const long long incl = block_scan(n, red, total);
-        if (r < r1) a.at[r] = (int)((unsigned)min((long long)INT_MAX, need_before + incl - n) | (replace ? 1u << 31 : 0u));
-        need_before += total;
-    }
-    const bool copy = a.refs_out != a.refs_in;
-    for (int base = p0; base < p1; base += kPlanThreads) {
-        const int p = base + tid;
-        int is_free = 0;
-        if (p < p1) {
-            const int c = __ldcg(&a.refs_in[p]);
-            is_free = c == 0;
-            if (copy) a.refs_out[p] = c;
+    // ---- 4. the records of the new and of the present rows (LOCAL: the first CTA's), and the lowest free pages in order
+    if (report) {
+        for (int r = ra; r < rb; ++r) {
+            const int n = need_of(r, x, replace, is_first);
+            const unsigned from = (unsigned)min((long long)INT_MAX, at) | (replace ? kTop : 0u);
+            a.rows[r] = make_int4(x.parent, x.keep, (int)((unsigned)x.room | (is_first ? kTop : 0u)), (int)from);
+            at += n;
         }
-        const long long incl = block_scan(is_free, red, total);
-        const long long spot = free_before + incl - 1;
-        if (is_free && ok && spot < need_all) a.free_ids[spot] = p;
-        free_before += total;
+        for (int p = start; p < a.Rin; p += stride) {
+            const int h = __ldcg(&a.held_lens[p]), cap = a.max_pages * kPageSize;
+            if (h < 0 || h > cap) bad |= kErrBadLength;
+            const int f = LOCAL ? first[p] : __ldcg(&first[p]);
+            int kept = 0;
+            if (f != INT_MAX) {
+                if constexpr (LOCAL) {
+                    kept = sm.keep[f];
+                } else {
+                    unsigned ignored = 0;
+                    Row y[1];
+                    load_rows(a, f, 1, y, ignored);
+                    kept = y[0].keep;
+                }
+            }
+            a.drops[p] = make_int2(cols(kept), cols(h < 0 ? 0 : (h > cap ? cap : h)));
+        }
+        if (bad) atomicOr(a.err, bad);
     }
+    if (ok) {
+        int pass = 0;
+        for (long long q = p0; q < p1 && free_before < need_all; q += kPass, ++pass) {
+            const long long mine = q + 1024 * warp;
+            unsigned w = pass < kWords ? words[0] : free_word(a.refs_in, wide, mine, p1);
+#pragma unroll
+            for (int i = 1; i < kWords; ++i) w = pass == i ? words[i] : w;
+            long long total, spot = free_before + block_scan(__popc(w), sm.red, total) - __popc(w);
+            for (; w && spot < need_all; w &= w - 1) a.free_ids[spot++] = (int)(mine + 32 * lane) + __ffs(w) - 1;
+            free_before += total;
+        }
+    }
+    cluster.barrier_wait(std::move(leave));
 }
 
-// Blocks [0, Rout) write the new rows, blocks [Rout, Rout + Rin) give up what the present rows held.  The counts
-// are only added to here (they may be the call's input): what depends on them was decided by the plan.
-__global__ void __launch_bounds__(kApplyThreads) fork_apply_kernel(const ForkArgs a) {
+template <int VEC>
+struct Pages {
+    int v[VEC];
+};
+template <int VEC>
+__device__ __forceinline__ Pages<VEC> load_pages(const int* p) {
+    Pages<VEC> x;
+    if constexpr (VEC == 4) {
+        const int4 y = __ldcg(reinterpret_cast<const int4*>(p));
+        x.v[0] = y.x;
+        x.v[1] = y.y;
+        x.v[2] = y.z;
+        x.v[3] = y.w;
+    } else if constexpr (VEC == 2) {
+        const int2 y = __ldcg(reinterpret_cast<const int2*>(p));
+        x.v[0] = y.x;
+        x.v[1] = y.y;
+    } else {
+        x.v[0] = __ldcg(p);
+    }
+    return x;
+}
+template <int VEC>
+__device__ __forceinline__ void store_pages(int* p, const Pages<VEC>& x) {
+    if constexpr (VEC == 4) *reinterpret_cast<int4*>(p) = make_int4(x.v[0], x.v[1], x.v[2], x.v[3]);
+    else if constexpr (VEC == 2) *reinterpret_cast<int2*>(p) = make_int2(x.v[0], x.v[1]);
+    else *p = x.v[0];
+}
+
+// Block b of `chunks` blocks a batch: columns kApplyThreads VEC (b % chunks) on, VEC a thread, of present and of new rows
+// kBatch (b / chunks) on.  The counts are only added to here (they may be the call's input): what depends on them was
+// decided by the plan.
+template <int VEC>
+__global__ void __launch_bounds__(kApplyThreads) fork_apply_kernel(const ForkArgs a, const int chunks) {
+    __shared__ int4 rows[kBatch];
+    __shared__ int2 drops[kBatch];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, batch = (int)(blockIdx.x / (unsigned)chunks), chunk = (int)(blockIdx.x % (unsigned)chunks);
+    const int b0 = batch * kBatch, c0 = (chunk * kApplyThreads + tid) * VEC;
+    const int n_out = min(kBatch, a.Rout - b0), n_in = min(kBatch, a.Rin - b0);  // may be negative
     const bool ok = __ldcg(a.ok) != 0;
-    unsigned bad = 0, ignored = 0;
-    if ((int)blockIdx.x < a.Rout) {
-        const int r = (int)blockIdx.x;
-        int* out = a.out_table + (long long)r * a.max_pages;
-        if (!ok) {
-            for (int c = tid; c < a.max_pages; c += kApplyThreads) out[c] = -1;
-            if (tid == 0) a.out_lens[r] = 0;
-            if (tid < 3) a.copies[3ll * r + tid] = tid < 2 ? -1 : 0;
-            return;
+    if (tid < n_out) rows[tid] = __ldcg(&a.rows[b0 + tid]);
+    if (tid >= 32 && tid - 32 < n_in) drops[tid - 32] = __ldcg(&a.drops[b0 + tid - 32]);
+    __syncthreads();
+    Pages<VEC> none;
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) none.v[v] = -1;
+    if (!ok) {
+        for (int i = 0; i < n_out; ++i) {
+            const long long r = b0 + i;
+            if (c0 < a.max_pages) store_pages<VEC>(&a.out_table[r * a.max_pages + c0], none);
+            if (chunk == 0 && tid == 0) a.out_lens[r] = 0;
+            if (chunk == 0 && tid < 3) a.copies[3 * r + tid] = tid < 2 ? -1 : 0;
         }
-        const Row x = row_of(a, r, ignored);
-        const int kc = cols(x.keep), rc = cols(x.room);
-        const unsigned plan = (unsigned)__ldcg(&a.at[r]);
-        const int replace = (int)(plan >> 31);
-        const int* fresh = a.free_ids + (plan & 0x7fffffffu) + replace - kc;  // the new page of column c is fresh[c]
-        const int* held = a.page_table + (long long)x.parent * a.max_pages;   // read where c < kc only
-        const bool first = x.parent >= 0 && __ldcg(&a.first[x.parent]) == r;
-        for (int c = tid; c < a.max_pages; c += kApplyThreads) {
-            int page = -1;
-            if (c < kc - replace) {
-                page = __ldcg(&held[c]);
-                if (page < 0 || page >= a.P) bad |= kErrBadPage;
-                else if (!first) atomicAdd(&a.refs_out[page], 1);
-            } else if (c < rc) {
-                page = __ldcg(&fresh[c]);
-                a.refs_out[page] = 1;
+        return;
+    }
+    unsigned bad = 0;
+    if (c0 < a.max_pages) {
+        // the columns that the present rows give up, and the pages of the new rows
+        Pages<VEC> old[kBatch], now[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            old[i] = none;
+            if (i < n_in && c0 + VEC > drops[i].x && c0 < drops[i].y)
+                old[i] = load_pages<VEC>(&a.page_table[(long long)(b0 + i) * a.max_pages + c0]);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            now[i] = none;
+            if (i >= n_out) continue;
+            const int4 x = rows[i];
+            const int replace = (int)((unsigned)x.w >> 31), kept = cols(x.y) - replace, rc = cols(x.z & 0x7fffffff);
+            if (c0 < kept) now[i] = load_pages<VEC>(&a.page_table[(long long)x.x * a.max_pages + c0]);
+            if (c0 + VEC > kept && c0 < rc) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    if (c0 + v >= kept && c0 + v < rc) now[i].v[v] = __ldcg(&a.free_ids[(x.w & 0x7fffffff) + c0 + v - kept]);
             }
-            out[c] = page;
         }
-        if (tid == 0) {
-            a.out_lens[r] = x.room;
-            int src = -1, dst = -1, tokens = 0;
-            if (replace) {
-                src = __ldcg(&held[kc - 1]);
-                dst = __ldcg(&fresh[kc - 1]);
-                tokens = x.keep % kPageSize;
-                if (first) atomicSub(&a.refs_out[src], 1);
+        // a column's changes, one after another, added up while they are of the same page
+        int page[VEC], change[VEC];
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            page[v] = -1;
+            change[v] = 0;
+        }
+        auto add = [&](int v, int p, int d) {
+            if (p != page[v]) {
+                if (change[v]) atomicAdd(&a.refs_out[page[v]], change[v]);
+                page[v] = p;
+                change[v] = 0;
             }
-            a.copies[3ll * r] = src;
-            a.copies[3ll * r + 1] = dst;
-            a.copies[3ll * r + 2] = tokens;
+            change[v] += d;
+        };
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i >= n_in || c0 + VEC <= drops[i].x || c0 >= drops[i].y) continue;
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                if (c0 + v < drops[i].x || c0 + v >= drops[i].y) continue;
+                if (old[i].v[v] < 0 || old[i].v[v] >= a.P) bad |= kErrBadPage;
+                else add(v, old[i].v[v], -1);
+            }
         }
-    } else if (ok) {
-        const int p = (int)blockIdx.x - a.Rout;
-        const int f = __ldcg(&a.first[p]);
-        const int from = f == INT_MAX ? 0 : cols(row_of(a, f, ignored).keep), to = cols(held_of(a, p));
-        const int* held = a.page_table + (long long)p * a.max_pages;
-        for (int c = from + tid; c < to; c += kApplyThreads) {
-            const int page = __ldcg(&held[c]);
-            if (page < 0 || page >= a.P) bad |= kErrBadPage;
-            else atomicSub(&a.refs_out[page], 1);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            if (i >= n_out) continue;
+            const int4 x = rows[i];
+            const int kept = cols(x.y) - (int)((unsigned)x.w >> 31), rc = cols(x.z & 0x7fffffff);
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                const int c = c0 + v, p = now[i].v[v];
+                if (c < kept) {
+                    if (p < 0 || p >= a.P) bad |= kErrBadPage;
+                    else if (x.z >= 0) add(v, p, 1);  // not the first child
+                } else if (c < rc) {
+                    a.refs_out[p] = 1;  // free until now: nothing else adds to it
+                } else {
+                    now[i].v[v] = -1;
+                }
+            }
+            store_pages<VEC>(&a.out_table[(long long)(b0 + i) * a.max_pages + c0], now[i]);
         }
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+            if (change[v]) atomicAdd(&a.refs_out[page[v]], change[v]);
+    }
+    if (chunk == 0 && tid < n_out) {
+        const int4 x = rows[tid];
+        const int kc = cols(x.y);
+        const bool replace = x.w < 0;
+        int src = -1, dst = -1, tokens = 0;
+        if (replace) {
+            src = __ldcg(&a.page_table[(long long)x.x * a.max_pages + kc - 1]);
+            dst = __ldcg(&a.free_ids[x.w & 0x7fffffff]);
+            tokens = x.y % kPageSize;
+            if (x.z < 0) atomicSub(&a.refs_out[src], 1);  // the first child does not go on in its parent's page
+        }
+        const long long r = b0 + tid;
+        a.out_lens[r] = x.z & 0x7fffffff;
+        a.copies[3 * r] = src;
+        a.copies[3 * r + 1] = dst;
+        a.copies[3 * r + 2] = tokens;
     }
     if (bad) atomicOr(a.err, bad);
 }
 
+// The plan's shared memory, allowed once per device and thread.
+cudaError_t allow_smem(const void* kernel, bool local, size_t bytes) {
+    static thread_local bool allowed[64][2] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && allowed[dev][local])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) allowed[dev][local] = true;
+    return e;
+}
+
 }  // namespace
 
-size_t fork_workspace(int Rin, int Rout, int P) { return (size_t(Rin) * 3 + size_t(Rout) + size_t(P) + 1) * 4; }
+void fork_plan(int Rin, int Rout, int P, ForkPlan* plan) {
+    auto up = [](size_t x) { return (x + 15) & ~size_t(15); };
+    plan->drops = up(size_t(Rout) * sizeof(int4));
+    plan->first = up(plan->drops + size_t(Rin) * sizeof(int2));
+    plan->low = up(plan->first + size_t(Rin) * 4);
+    plan->high = up(plan->low + size_t(Rin) * 4);
+    plan->free_ids = up(plan->high + size_t(Rin) * 4);
+    plan->ok = up(plan->free_ids + size_t(P) * 4);
+    plan->ws_bytes = plan->ok + 4;
+}
 
 cudaError_t pages_fork_launch(const ForkArgs& a, cudaStream_t stream) {
-    // one CTA while a row or page or two per thread are all there is, else a cluster of eight
-    const int most = a.Rin > a.Rout ? (a.Rin > a.P ? a.Rin : a.P) : (a.Rout > a.P ? a.Rout : a.P);
-    const int ctas = most <= 2 * kPlanThreads ? 1 : 8;
+    // one CTA while a row or a step of pages per thread are all there is, else a cluster of eight
+    const int ctas = a.Rin <= kPlanThreads && a.Rout <= kPlanThreads && a.P <= 4 * kPlanThreads ? 1 : 8;
+    const bool local = a.Rin <= kLocalRows && a.Rout <= kLocalRows;
+    void (*plan)(const ForkArgs) = local ? fork_plan_kernel<true> : fork_plan_kernel<false>;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(plan), local, sizeof(PlanSmem));
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -268,17 +516,30 @@ cudaError_t pages_fork_launch(const ForkArgs& a, cudaStream_t stream) {
     attr[1].val.clusterDim.x = (unsigned)ctas;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
+    // behind the planning cluster, clusters that copy the counts, four steps of a thread each
+    const int copiers = a.refs_out == a.refs_in ? 0 : (a.P / (16 * kPlanThreads * ctas) < 16 ? a.P / (16 * kPlanThreads * ctas) + 1 : 16);
+    cfg.gridDim = dim3((unsigned)(ctas * (1 + copiers)));
     cfg.blockDim = dim3(kPlanThreads);
+    cfg.dynamicSmemBytes = sizeof(PlanSmem);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, fork_plan_kernel, a);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3((unsigned)(a.Rout + a.Rin));
+    if ((e = cudaLaunchKernelEx(&cfg, plan, a)) != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
+    const int rows = a.Rin > a.Rout ? a.Rin : a.Rout;
+    if (rows == 0) return cudaSuccess;
+    // as many columns a thread as every row of both tables allows loads of
+    const bool even = ((reinterpret_cast<uintptr_t>(a.page_table) | reinterpret_cast<uintptr_t>(a.out_table)) & 15) == 0;
+    const int vec = !even ? 1 : (a.max_pages % 4 == 0 ? 4 : (a.max_pages % 2 == 0 ? 2 : 1));
+    const int chunks = (a.max_pages + kApplyThreads * vec - 1) / (kApplyThreads * vec);
+    const long long blocks = (long long)((rows + kBatch - 1) / kBatch) * chunks;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3((unsigned)blocks);
     cfg.blockDim = dim3(kApplyThreads);
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fork_apply_kernel, a);
+    return vec == 4   ? cudaLaunchKernelEx(&cfg, fork_apply_kernel<4>, a, chunks)
+           : vec == 2 ? cudaLaunchKernelEx(&cfg, fork_apply_kernel<2>, a, chunks)
+                      : cudaLaunchKernelEx(&cfg, fork_apply_kernel<1>, a, chunks);
 }
 
 }  // namespace sinkattn

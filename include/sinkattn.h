@@ -456,7 +456,7 @@ sinkattn_status_t sinkattn_beam_select(const void *logits, const float *scores, 
 typedef struct {
     int32_t num_rows_in;       /* rows of the present page table, 0..2^20                 */
     int32_t num_rows_out;      /* rows of the new page table, 0..2^20                     */
-    int32_t num_pages;         /* P, pages of the pool                                    */
+    int32_t num_pages;         /* P, pages of the pool, 0..2^30                           */
     int32_t max_pages;         /* row length of both page tables (>= 1)                   */
     int32_t page_size;         /* must be 16                                              */
     int32_t grow;              /* room for new tokens per row where room_lens is NULL (>= 0) */

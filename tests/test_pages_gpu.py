@@ -347,3 +347,53 @@ def test_move_refusals(S):
     with pytest.raises(ValueError):
         S.sinkattn_kv_compact(k, v, ints([[0], [1]]), ints([0]), ints([[1]]), ints([1]))
     S.sinkattn_kv_copy(k, v, torch.empty(0, 3, dtype=torch.int32, device="cuda"))  # nothing to do
+
+
+def test_more_rows_than_one_cta_keeps(S):
+    """Over 4096 rows the plan is made by parts, with the parents' children in the workspace."""
+    rng = random.Random(6)
+    rows, mp, P = 9000, 3, 40001
+    ids = rng.sample(range(P), P)
+    held = [rng.randint(0, 40) for _ in range(rows)]
+    table, refs = [], [0] * P
+    for n in held:
+        row = [ids.pop() for _ in range(cols(n))]
+        if table and rng.random() < 0.3 and row and table[-1]:
+            row[0] = table[-1][0]
+        table.append(row)
+        for p in row:
+            refs[p] += 1
+    for R in (4097, 12000):
+        parents = [rng.randint(-1, rows - 1) for _ in range(R)]
+        keep = [rng.randint(0, held[p]) if p >= 0 and rng.random() < 0.3 else (held[p] if p >= 0 else 0) for p in parents]
+        room = [min(mp * PS, k + rng.randint(0, 3)) for k in keep]
+        got = call(S, table, mp, held, parents, refs, keep, room)
+        assert S.sinkattn_get_error() == 0
+        same(got, fork_reference_fast(table, held, parents, refs, keep, room), mp)
+
+
+def fork_reference_fast(table, held, parents, refs, keep, room):
+    """fork_reference with every parent's children collected first (thousands of rows)."""
+    kids = {}
+    for r, p in enumerate(parents):
+        kids.setdefault(p, []).append(r)
+    writes = [m > k and k % PS != 0 for k, m in zip(keep, room)]
+    free = iter([p for p, c in enumerate(refs) if c == 0])
+    new_table, copies, counts = [], [], list(refs)
+    for r, p in enumerate(parents):
+        kept, copy = (table[p][:cols(keep[r])] if p >= 0 else []), (-1, -1, 0)
+        if writes[r]:
+            mates = kids[p]
+            if not (refs[kept[-1]] == 1 and mates[0] == r and all(writes[q] and keep[q] == keep[r] for q in mates)):
+                copy = (kept[-1], next(free), keep[r] % PS)
+                kept = kept[:-1] + [copy[1]]
+        kept = kept + [next(free) for _ in range(cols(room[r]) - len(kept))]
+        new_table.append(kept)
+        copies.append(copy)
+    for p in range(len(table)):
+        for c in range(cols(held[p])):
+            counts[table[p][c]] -= 1
+    for row in new_table:
+        for page in row:
+            counts[page] += 1
+    return new_table, room, counts, copies
