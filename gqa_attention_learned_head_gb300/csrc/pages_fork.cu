@@ -15,9 +15,9 @@
 // (through distributed shared memory) have said where each thread's free pages go.  Its time is latency: chains of
 // loads (a row's parent, its parent's tokens, its last page, that page's count) and barriers.  So up to kLocalRows
 // rows every CTA goes over all of them by itself, in shared memory, and the cluster meets once.
-// fork_apply_kernel: a thread takes one column of kBatch present and kBatch new rows, reads and writes their
-// entries, and adds up the changes to a page's count as long as neighbouring rows hold the same page: for the pages
-// that a group's rows share, drops and forks mostly cancel and no atomic is left.  Bound by the table's bytes.
+// fork_apply_kernel: a thread takes a column or some of kBatch present and kBatch new rows, reads and writes their
+// entries, and adds up the changes to the count of a page that several of them hold: for the pages that a group's
+// rows share, drops and forks mostly cancel and no atomic is left.  Bound by the table's bytes.
 #include "args_pages.h"
 #include "ptx.cuh"
 
@@ -359,21 +359,57 @@ __device__ __forceinline__ void store_pages(int* p, const Pages<VEC>& x) {
     else *p = x.v[0];
 }
 
+// A new row as the apply kernel uses it: columns [0, kept) from its parent's row, [kept, rc) new pages.
+struct ApplyRow {
+    const int* from;   // its parent's row
+    const int* fresh;  // fresh[c] is column c's new page
+    int kept, rc;
+};
+// The pages of columns [begin, end) of a row lose or gain a holder.
+struct Change {
+    const int* row;
+    int begin, end, by;
+};
+
 // Block b of `chunks` blocks a batch: columns kApplyThreads VEC (b % chunks) on, VEC a thread, of present and of new rows
 // kBatch (b / chunks) on.  The counts are only added to here (they may be the call's input): what depends on them was
 // decided by the plan.
 template <int VEC>
 __global__ void __launch_bounds__(kApplyThreads) fork_apply_kernel(const ForkArgs a, const int chunks) {
-    __shared__ int4 rows[kBatch];
-    __shared__ int2 drops[kBatch];
+    __shared__ ApplyRow rows[kBatch];
+    __shared__ Change changes[2 * kBatch];
+    __shared__ int num_changes;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tid = threadIdx.x, batch = (int)(blockIdx.x / (unsigned)chunks), chunk = (int)(blockIdx.x % (unsigned)chunks);
-    const int b0 = batch * kBatch, c0 = (chunk * kApplyThreads + tid) * VEC;
+    // the block's columns [lo, hi) (as if whole) and the thread's first
+    const int b0 = batch * kBatch, lo = chunk * kApplyThreads * VEC, hi = lo + kApplyThreads * VEC, c0 = lo + tid * VEC;
     const int n_out = min(kBatch, a.Rout - b0), n_in = min(kBatch, a.Rin - b0);  // may be negative
     const bool ok = __ldcg(a.ok) != 0;
-    if (tid < n_out) rows[tid] = __ldcg(&a.rows[b0 + tid]);
-    if (tid >= 32 && tid - 32 < n_in) drops[tid - 32] = __ldcg(&a.drops[b0 + tid - 32]);
+    int4 mine = make_int4(-1, 0, 0, 0);
+    ApplyRow x = {nullptr, nullptr, 0, 0};
+    if (tid < 32) {
+        // lanes 0 .. kBatch - 1 the new rows, the next ones the present rows; the changes that touch this block, losses first
+        Change y = {nullptr, 0, 0, 0};
+        const int i = tid - kBatch;
+        if (tid < n_out) {
+            mine = __ldcg(&a.rows[b0 + tid]);
+            x.kept = cols(mine.y) - (int)((unsigned)mine.w >> 31);
+            x.rc = cols(mine.z & 0x7fffffff);
+            x.from = a.page_table + (long long)mine.x * a.max_pages;
+            x.fresh = a.free_ids + (mine.w & 0x7fffffff) - x.kept;
+            rows[tid] = x;
+            if (mine.z >= 0) y = Change{x.from, 0, x.kept, 1};  // not its parent's first child
+        } else if (i >= 0 && i < n_in) {
+            const int2 d = __ldcg(&a.drops[b0 + i]);
+            y = Change{a.page_table + (long long)(b0 + i) * a.max_pages, d.x, d.y, -1};
+        }
+        const bool here = y.end > lo && y.begin < hi && y.end > y.begin;
+        const unsigned below = (1u << tid) - 1, gains = __ballot_sync(0xffffffffu, here && y.by > 0),
+                       losses = __ballot_sync(0xffffffffu, here && y.by < 0);
+        if (here) changes[y.by < 0 ? __popc(losses & below) : __popc(losses) + __popc(gains & below)] = y;
+        if (tid == 0) num_changes = __popc(losses | gains);
+    }
     __syncthreads();
     Pages<VEC> none;
 #pragma unroll
@@ -387,95 +423,95 @@ __global__ void __launch_bounds__(kApplyThreads) fork_apply_kernel(const ForkArg
         }
         return;
     }
-    unsigned bad = 0;
+    bool bad = false;
     if (c0 < a.max_pages) {
-        // the columns that the present rows give up, and the pages of the new rows
-        Pages<VEC> old[kBatch], now[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            old[i] = none;
-            if (i < n_in && c0 + VEC > drops[i].x && c0 < drops[i].y)
-                old[i] = load_pages<VEC>(&a.page_table[(long long)(b0 + i) * a.max_pages + c0]);
-        }
+        // ---- the new rows' entries
+        Pages<VEC> now[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             now[i] = none;
-            if (i >= n_out) continue;
-            const int4 x = rows[i];
-            const int replace = (int)((unsigned)x.w >> 31), kept = cols(x.y) - replace, rc = cols(x.z & 0x7fffffff);
-            if (c0 < kept) now[i] = load_pages<VEC>(&a.page_table[(long long)x.x * a.max_pages + c0]);
-            if (c0 + VEC > kept && c0 < rc) {
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    if (c0 + v >= kept && c0 + v < rc) now[i].v[v] = __ldcg(&a.free_ids[(x.w & 0x7fffffff) + c0 + v - kept]);
-            }
+            if (i < n_out && c0 < rows[i].kept) now[i] = load_pages<VEC>(rows[i].from + c0);
         }
-        // a column's changes, one after another, added up while they are of the same page
-        int page[VEC], change[VEC];
+        // ---- the first changes' pages, on their way meanwhile
+        const int n = num_changes;
+        Pages<VEC> at[kBatch];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            page[v] = -1;
-            change[v] = 0;
-        }
-        auto add = [&](int v, int p, int d) {
-            if (p != page[v]) {
-                if (change[v]) atomicAdd(&a.refs_out[page[v]], change[v]);
-                page[v] = p;
-                change[v] = 0;
-            }
-            change[v] += d;
-        };
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-            if (i >= n_in || c0 + VEC <= drops[i].x || c0 >= drops[i].y) continue;
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                if (c0 + v < drops[i].x || c0 + v >= drops[i].y) continue;
-                if (old[i].v[v] < 0 || old[i].v[v] >= a.P) bad |= kErrBadPage;
-                else add(v, old[i].v[v], -1);
-            }
+        for (int e = 0; e < kBatch; ++e) {
+            at[e] = none;
+            if (e < n && c0 < changes[e].end) at[e] = load_pages<VEC>(changes[e].row + c0);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            if (i >= n_out) continue;
-            const int4 x = rows[i];
-            const int kept = cols(x.y) - (int)((unsigned)x.w >> 31), rc = cols(x.z & 0x7fffffff);
+            if (i >= n_out) break;
+            if (hi > rows[i].kept) {  // new pages, or nothing, in some of the block's columns
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const int c = c0 + v, p = now[i].v[v];
-                if (c < kept) {
-                    if (p < 0 || p >= a.P) bad |= kErrBadPage;
-                    else if (x.z >= 0) add(v, p, 1);  // not the first child
-                } else if (c < rc) {
-                    a.refs_out[p] = 1;  // free until now: nothing else adds to it
-                } else {
-                    now[i].v[v] = -1;
+                for (int v = 0; v < VEC; ++v) {
+                    const int c = c0 + v;
+                    if (c < rows[i].kept) {
+                        bad |= (unsigned)now[i].v[v] >= (unsigned)a.P;
+                    } else if (c < rows[i].rc) {
+                        now[i].v[v] = __ldcg(rows[i].fresh + c);
+                        a.refs_out[now[i].v[v]] = 1;  // free until now: nothing else adds to it
+                    } else {
+                        now[i].v[v] = -1;
+                    }
                 }
+            } else {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) bad |= (unsigned)now[i].v[v] >= (unsigned)a.P;
             }
             store_pages<VEC>(&a.out_table[(long long)(b0 + i) * a.max_pages + c0], now[i]);
         }
+        // ---- the changes of a column, one after another, added up while they are of the same page
+        int page[VEC], sum[VEC];
 #pragma unroll
-        for (int v = 0; v < VEC; ++v)
-            if (change[v]) atomicAdd(&a.refs_out[page[v]], change[v]);
+        for (int v = 0; v < VEC; ++v) page[v] = sum[v] = 0;
+        auto flush = [&](int v) {
+            if (sum[v]) atomicAdd(&a.refs_out[page[v]], sum[v]);
+            sum[v] = 0;
+        };
+        auto add = [&](const Change& y, const Pages<VEC>& p) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) {
+                if (c0 + v < y.begin || c0 + v >= y.end) continue;
+                if ((unsigned)p.v[v] >= (unsigned)a.P) {
+                    bad = true;
+                    continue;
+                }
+                if (p.v[v] != page[v]) {
+                    flush(v);
+                    page[v] = p.v[v];
+                }
+                sum[v] += y.by;
+            }
+        };
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+            if (e >= n) break;
+            add(changes[e], at[e]);
+        }
+#pragma unroll 1
+        for (int e = kBatch; e < n; ++e)
+            if (c0 < changes[e].end) add(changes[e], load_pages<VEC>(changes[e].row + c0));
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) flush(v);
     }
     if (chunk == 0 && tid < n_out) {
-        const int4 x = rows[tid];
-        const int kc = cols(x.y);
-        const bool replace = x.w < 0;
+        const bool replace = mine.w < 0;
         int src = -1, dst = -1, tokens = 0;
         if (replace) {
-            src = __ldcg(&a.page_table[(long long)x.x * a.max_pages + kc - 1]);
-            dst = __ldcg(&a.free_ids[x.w & 0x7fffffff]);
-            tokens = x.y % kPageSize;
-            if (x.z < 0) atomicSub(&a.refs_out[src], 1);  // the first child does not go on in its parent's page
+            src = __ldcg(x.from + x.kept);
+            dst = __ldcg(x.fresh + x.kept);
+            tokens = mine.y % kPageSize;
+            if (mine.z < 0) atomicSub(&a.refs_out[src], 1);  // the first child does not go on in its parent's page
         }
         const long long r = b0 + tid;
-        a.out_lens[r] = x.z & 0x7fffffff;
+        a.out_lens[r] = mine.z & 0x7fffffff;
         a.copies[3 * r] = src;
         a.copies[3 * r + 1] = dst;
         a.copies[3 * r + 2] = tokens;
     }
-    if (bad) atomicOr(a.err, bad);
+    if (bad) atomicOr(a.err, kErrBadPage);
 }
 
 // The plan's shared memory, allowed once per device and thread.
