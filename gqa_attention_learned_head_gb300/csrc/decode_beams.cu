@@ -78,17 +78,20 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
 
     int id[KMAX];       // the column's page of each row, -1 where it has none
     unsigned set[KMAX]; // the rows that hold the same page, for the first of them; else 0
-    auto column = [&](int c, bool report) {
+    bool bad = false;
+    auto column = [&](int c) {
+        auto holds = [&](int k) { return k < K && c < c1 && c * kPageSize < len[k]; };
+#pragma unroll
+        for (int k = 0; k < KMAX; ++k)  // every row's load before any is looked at
+            id[k] = holds(k) ? __ldcg(&table[(long long)k * a.max_pages + c]) : -1;
+        int distinct = 0;
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
-            id[k] = -1;
-            if (k < K && c < c1 && c * kPageSize < len[k]) {
-                const int page = __ldcg(&table[(long long)k * a.max_pages + c]);
-                if (page >= 0 && page < a.num_pages) id[k] = page;
-                else if (report) atomicOr(a.err, kErrBadPage);
+            if (id[k] < 0 || id[k] >= a.num_pages) {
+                bad |= holds(k);
+                id[k] = -1;
             }
         }
-        int distinct = 0;
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
             unsigned same = 0;
@@ -122,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
     int at = 0, total;
     if (ctas > 1) {
         int mine = 0;
-        for (int c = c0 + tid; c < c1; c += kPlanThreads) mine += column(c, false);
+        for (int c = c0 + tid; c < c1; c += kPlanThreads) mine += column(c);
         (void)block_sum(mine, total);
         if (tid == 0) counted = total;
         cluster.sync();
@@ -131,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
     }
     PageEntry* out = a.entries + (long long)n * K * a.max_pages;
     for (int base = c0; base < c1; base += kPlanThreads) {
-        const int c = base + tid, distinct = column(c, true);
+        const int c = base + tid, distinct = column(c);
         int to = at + block_sum(distinct, total);
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
@@ -145,6 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
         }
         at += total;
     }
+    if (bad) atomicOr(a.err, kErrBadPage);
     if (rank == ctas - 1 && tid == 0) a.counts[n] = at;
 }
 
