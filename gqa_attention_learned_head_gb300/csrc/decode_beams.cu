@@ -167,6 +167,13 @@ struct Piece {
     long long seg_start;
 };
 
+// The entry of lane l's page (l & 7) of tile t, or, where the segment has no such page, its last: read all the same, so
+// that the load stays in flight until its value is needed (a choice made on the value would wait for it at once).
+__device__ __forceinline__ int tile_entry(const Piece& p, int t, int lane) {
+    const int i = t * kPagesPerTile + (lane & 7);
+    return i < p.pages ? i : p.pages - 1;
+}
+
 // Walks the pieces of units [x, x1); every role of the CTA runs its own walker over the same share.
 struct Walk {
     int b, g, tiles, pages;
@@ -206,14 +213,33 @@ struct __align__(1024) Smem {
     uint8_t k[kKStages][kTileBytes];
     uint8_t v[kVStages][kTileBytes];
     uint64_t q_full[2], q_empty[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-    uint64_t s_full, s_free, p_full, o_done, mma_done;
+    uint64_t s_full, s_free, p_full, o_done, mma_done, exchange;
     uint32_t tmem_base;
     long long red[8];    // block reductions
     long long found[4];  // share start: group, its first unit, its tiles, flag
     Walk walk[4];        // the softmax warps' walkers (kept out of their registers)
     Piece piece[4];      // ... and their current pieces
+    int4 entry[4][2][kPagesPerTile];  // ... and their pages' entries, this tile's and the next one's
+    float2 md[kBM];                   // SPLIT > 1: running maximum and normaliser of every thread at a piece's end
+    float half[16][kBM];              // SPLIT = 4: the second exchange of partial sums
 };
 
+// cp.async of 16 bytes through L2, and the wait for all of a thread's.
+__device__ __forceinline__ void copy16_async(void* smem, const void* gmem) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem)), "l"(gmem) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+
+template <int SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_beams_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const BeamsArgs a) {
@@ -221,14 +247,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.N, Hkv = a.Hkv, R = a.R, K = a.K, G = a.G;
-    const int active = (R + 31) / 32;  // softmax warps that hold rows
+    constexpr int kKeys = kBN / SPLIT;  // keys of a tile that a softmax thread takes
+    constexpr int kBlock = kBM / SPLIT;  // rows of a copy of the query rows
+    const int active = SPLIT > 1 ? 4 : (R + 31) / 32;  // softmax warps that hold rows
 
     // ---- 0. set-up that reads no input (barriers, tensor memory, the Q padding): done before the wait
     // below, so it overlaps the preceding kernel's tail
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.q_full[i], 1);
-            mbar_init(&sm.q_empty[i], 1);
+            mbar_init(&sm.q_empty[i], SPLIT > 1 ? 1 + 128 : 1);
         }
         for (int i = 0; i < kKStages; ++i) {
             mbar_init(&sm.k_full[i], 1);
@@ -243,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(&sm.p_full, 32 * active);
         mbar_init(&sm.o_done, 1);
         mbar_init(&sm.mma_done, 2);
+        mbar_init(&sm.exchange, 128);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
@@ -250,8 +279,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_alloc(&sm.tmem_base, kTmemCols);
         tmem_relinquish();
     }
-    // Q rows R..127 (no query) are zeros, so their scores stay finite; the TMA writes rows 0..R-1
-    for (int e = R * 8 + tid; e < kBM * 8; e += kThreads) {
+    // rows without a query start as zeros; the TMA writes the first R rows of every copy
+    for (int e = tid; e < kBM * 8; e += kThreads) {
+        if ((e >> 3) % kBlock < R) continue;
         reinterpret_cast<uint4*>(sm.q[0])[e] = make_uint4(0u, 0u, 0u, 0u);
         reinterpret_cast<uint4*>(sm.q[1])[e] = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -376,7 +406,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tbase = sm.tmem_base;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // 128 x kFew + 128 x kMany = 256 x 128, the launch's registers: a thread's scores of a whole tile want many
+        constexpr int kFew = SPLIT > 1 ? 96 : 80;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFew));
         if (warp == 0 || warp == 3) {
             // ------------------------------------------------------------ TMA producers
             const bool is_k = warp == 0;
@@ -397,19 +429,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (lane == 0) {
                         if (p >= 2) got = mbar_wait(&sm.q_empty[p & 1], ((p >> 1) - 1) & 1);
                         if (got) {
-                            mbar_arrive_expect_tx(&sm.q_full[p & 1], (uint32_t)R * 128u);
-                            tma_load_3d(sm.q[p & 1], &tmap_q, 0, pc.g * G, pc.b * K, &sm.q_full[p & 1]);
+                            mbar_arrive_expect_tx(&sm.q_full[p & 1], (uint32_t)(SPLIT * R) * 128u);
+#pragma unroll
+                            for (int c = 0; c < SPLIT; ++c)
+                                tma_load_3d(sm.q[p & 1] + c * kBlock * 128, &tmap_q, 0, pc.g * G, pc.b * K, &sm.q_full[p & 1]);
                         }
                     }
                     if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
                 }
                 ++p;
                 // page ids (lanes 0-7), read one tile ahead of the copies
-                auto page_of = [&](int t) {
-                    const int i = t * kPagesPerTile + (lane & 7);
-                    return i < pc.pages ? entry_of(a, pc.b, i).page : -1;
-                };
-                int page = page_of(pc.ta);
+                int page = entry_of(a, pc.b, tile_entry(pc, pc.ta, lane)).page;
                 for (int t = pc.ta; ok && t < pc.tb; ++t, ++J) {
                     const int st = J % stages;
                     if (J >= stages) {
@@ -418,8 +448,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (!(ok = __shfl_sync(0xffffffffu, got, 0) != 0)) break;
                     }
                     // a tile's missing pages are copied from behind the pool's end: zeros
-                    const int row = page < 0 ? a.num_pages * Hkv * kPageSize : (page * Hkv + pc.g) * kPageSize;
-                    if (t + 1 < pc.tb) page = page_of(t + 1);
+                    const int row = t * kPagesPerTile + lane < pc.pages ? (page * Hkv + pc.g) * kPageSize
+                                                                        : a.num_pages * Hkv * kPageSize;
+                    page = entry_of(a, pc.b, tile_entry(pc, t + 1, lane)).page;
                     if (lane == 0) mbar_arrive_expect_tx(&full[st], kTileBytes);
                     __syncwarp();
                     uint8_t* tile = is_k ? sm.k[st] : sm.v[st];
@@ -472,28 +503,27 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool ok = true;
             Piece pc;
             while (ok && walk.next(a, pc)) {
-                auto slots_of = [&](int t) {
-                    const int i = t * kPagesPerTile + (lane & 7);
-                    return i < pc.pages ? entry_of(a, pc.b, i).slots & ~kAllSee : kPageSize;  // missing: zeros already
-                };
-                int slots = slots_of(pc.ta);
+                int slots = entry_of(a, pc.b, tile_entry(pc, pc.ta, lane)).slots;  // read one tile ahead
                 for (int t = pc.ta; t < pc.tb; ++t, ++J) {
                     const int st = J % kVStages;
                     ok = warp_wait(&sm.v_full[st], (J / kVStages) & 1);
                     if (!ok) break;
-                    uint32_t part = __ballot_sync(0xffffffffu, lane < kPagesPerTile && slots < kPageSize);
+                    // (the slots of missing pages are zeros already)
+                    const int filled = slots & ~kAllSee;
+                    uint32_t part = __ballot_sync(0xffffffffu, lane < kPagesPerTile && t * kPagesPerTile + lane < pc.pages &&
+                                                                   filled < kPageSize);
+                    slots = entry_of(a, pc.b, tile_entry(pc, t + 1, lane)).slots;
                     if (part) {
                         while (part) {
                             const int pg = __ffs(part) - 1;
                             part &= part - 1;
-                            const int n = __shfl_sync(0xffffffffu, slots, pg);
+                            const int n = __shfl_sync(0xffffffffu, filled, pg);
                             for (int e = (pg * kPageSize + n) * 8 + lane; e < (pg + 1) * kPageSize * 8; e += 32)
                                 reinterpret_cast<uint4*>(sm.v[st])[e] = make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
-                    if (t + 1 < pc.tb) slots = slots_of(t + 1);
                     if (!(ok = warp_wait(&sm.p_full, J & 1))) break;
                     tc_fence_after();
                     const uint32_t vaddr = smem_u32(sm.v[st]);
@@ -512,18 +542,25 @@ __global__ void __launch_bounds__(kThreads, 2)
             (void)warp_wait(&sm.mma_done, 0);
         }
     } else {
-        // 128 x 56 + 128 x 200 = 256 x 128, the launch's registers
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        const int r = tid - 128;
+        constexpr int kMany = SPLIT > 1 ? 160 : 176;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMany));
+        const int copy = (tid - 128) / kBlock, r = (tid - 128) % kBlock;  // copy of the query rows, row
         const bool live = r < R;
         const int i = live ? r / G : 0, h = live ? r % G : 0;
         int2 head = make_int2(-1, 0);  // the share's last piece, if it starts a segment it does not end
         if (warp - 4 < active) {
             // ---------------------------------------------------------------- softmax
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t tS = tbase + lane_off + kColS, tO = tbase + lane_off + kColO, tP = tbase + lane_off + kColP;
+            const uint32_t tS = tbase + lane_off + kColS + copy * kKeys, tO = tbase + lane_off + kColO;
+            const uint32_t tP = tbase + lane_off + kColP;
             const float scale_log2 = a.scale_log2;
-            int J = 0;
+            if constexpr (SPLIT > 1) {  // the weights of the keys that other copies take stay zero
+                uint32_t zero[32] = {};
+                tmem_st32(tP, zero);
+                tmem_st32(tP + 32, zero);
+                tc_wait_st();
+            }
+            int J = 0, p = 0, ex = 0;  // tiles, pieces, phases of the exchange barrier
             bool ok = true;
             const int sw = warp - 4;
             if (lane == 0) sm.walk[sw] = walk;
@@ -535,41 +572,52 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!__shfl_sync(0xffffffffu, has, 0)) break;
                 __syncwarp();
                 const Piece& pc = sm.piece[sw];
+                const int ta = pc.ta, tb = pc.tb, pages = pc.pages;
+                const PageEntry* entries = a.entries + (long long)pc.b * K * a.max_pages;
+                // the entries of a tile's pages are copied to shared memory one tile ahead (in registers they would not fit
+                // beside the scores, and a spill waits for the load)
+                auto fetch = [&](int t) {
+                    if (lane < kPagesPerTile) {
+                        const int e = t * kPagesPerTile + lane;
+                        copy16_async(&sm.entry[sw][t & 1][lane], entries + (e < pages ? e : pages - 1));
+                    }
+                };
+                fetch(ta);
                 // this row's cached tokens (the plan kernel reported lengths out of range)
                 const int len = live ? clamp_len(__ldcg(&a.kv_lens[(long long)pc.b * K + i]), a.max_pages * kPageSize) : 0;
-                const int ta = pc.ta, tb = pc.tb;
-                const bool seeded = ta == 0;
+                const bool seeded = ta == 0 && copy == 0;
                 float m = (seeded && live) ? __ldg(&a.sinks[pc.g * G + h]) * kLog2e : kNegInf;
                 float d = (seeded && live) ? 1.f : 0.f;  // the sink's own e^(sink - m) = 1
-                // a tile's page entries (lanes 0-7), read one tile ahead
-                auto load_entry = [&](int t) {
-                    const int e = t * kPagesPerTile + (lane & 7);
-                    return e < pc.pages ? entry_of(a, pc.b, e) : PageEntry{-1, 0, 0u, 0};
-                };
-                PageEntry entry = load_entry(ta);
                 for (int t = ta; t < tb; ++t, ++J) {
-                    const bool masked = !__all_sync(0xffffffffu, (entry.slots & kAllSee) != 0);
-                    // this row's visible keys of the tile: of each page, the slots its length reaches
-                    uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                    copies_done();
+                    __syncwarp();
+                    const int4* entry = sm.entry[sw][t & 1];
+                    fetch(t + 1);
+                    // does any row of this warp's keys' pages see less than all of them?
+                    constexpr int kMine = kKeys / kPageSize;  // pages of this copy's keys
+                    const int page0 = copy * kMine, left = pages - t * kPagesPerTile - page0;
+                    const bool masked =
+                        left < kMine || !__all_sync(0xffffffffu, (entry[page0 + lane % kMine].w & kAllSee) != 0);
+                    // this row's visible keys: of each page, the slots its length reaches
+                    uint32_t vis[kKeys / 32];
                     if (masked) {
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) {
+                        for (int w = 0; w < kKeys / 32; ++w) {
                             vis[w] = 0u;
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
-                                const uint32_t beams = __shfl_sync(0xffffffffu, entry.beams, 2 * w + half);
-                                const int n = len - kPageSize * __shfl_sync(0xffffffffu, entry.col, 2 * w + half);
+                                const int4 e = entry[page0 + 2 * w + half];
+                                const int n = len - kPageSize * e.y;
                                 const uint32_t bits = n >= kPageSize ? 0xFFFFu : (n > 0 ? (1u << n) - 1u : 0u);
-                                if (live && ((beams >> i) & 1u)) vis[w] |= bits << (16 * half);
+                                if (live && 2 * w + half < left && (((uint32_t)e.z >> i) & 1u)) vis[w] |= bits << (16 * half);
                             }
                         }
                     }
-                    if (t + 1 < tb) entry = load_entry(t + 1);
                     if (!(ok = warp_wait(&sm.s_full, J & 1))) break;
                     tc_fence_after();
-                    float s[128];
+                    float s[kKeys];
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc)
+                    for (int cc = 0; cc < kKeys / 32; ++cc)
                         tmem_ld32(tS + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&s[cc * 32]));
                     tc_wait_ld();
                     tc_fence_before();
@@ -578,22 +626,22 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float mul = scale_log2;
                     if (!(scale_log2 > 0.f)) {  // zero or negative scale: scale first, mask after
 #pragma unroll
-                        for (int cc = 0; cc < 128; ++cc) s[cc] *= scale_log2;
+                        for (int cc = 0; cc < kKeys; ++cc) s[cc] *= scale_log2;
                         mul = 1.f;
                     }
                     if (masked) {
 #pragma unroll
-                        for (int cc = 0; cc < 128; ++cc) s[cc] = ((vis[cc >> 5] >> (cc & 31)) & 1u) ? s[cc] : kNegInf;
+                        for (int cc = 0; cc < kKeys; ++cc) s[cc] = ((vis[cc >> 5] >> (cc & 31)) & 1u) ? s[cc] : kNegInf;
                     }
                     float acc[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) acc[e] = fmax3(s[e], s[8 + e], s[16 + e]);
 #pragma unroll
-                    for (int cc = 24; cc < 120; cc += 16)
+                    for (int cc = 24; cc < kKeys - 8; cc += 16)
 #pragma unroll
                         for (int e = 0; e < 8; ++e) acc[e] = fmax3(acc[e], s[cc + e], s[cc + 8 + e]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], s[120 + e]);
+                    for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], s[kKeys - 8 + e]);
                     const float mx_raw =
                         fmaxf(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], fmax3(acc[5], acc[6], acc[7])));
                     const float mx = mx_raw == kNegInf ? kNegInf : mx_raw * mul;
@@ -611,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float2 mul2 = make_float2(mul, mul), negm2 = make_float2(neg_m, neg_m);
                     float2 sums[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                                       make_float2(0.f, 0.f)};
-                    uint32_t pk[64];
+                    uint32_t pk[kKeys / 2];
 #pragma unroll
-                    for (int cc = 0; cc < 64; ++cc) {
+                    for (int cc = 0; cc < kKeys / 2; ++cc) {
                         const float2 xx = ffma2(make_float2(s[2 * cc], s[2 * cc + 1]), mul2, negm2);
                         const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
                         sums[cc & 3] = fadd2(sums[cc & 3], pp);
@@ -636,53 +684,109 @@ __global__ void __launch_bounds__(kThreads, 2)
                             }
                         }
                     }
-                    tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-                    tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+                    if constexpr (SPLIT == 4) {
+                        tmem_st16(tP + copy * 16, pk);
+                    } else {
+#pragma unroll
+                        for (int cc = 0; cc < kKeys / 64; ++cc)
+                            tmem_st32(tP + copy * (kKeys / 2) + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[cc * 32]));
+                    }
                     tc_wait_st();
                     tc_fence_before();
                     mbar_arrive(&sm.p_full);
                 }
+                copies_done();  // the entries fetched last land before their slot is fetched into again
+                __syncwarp();
                 if (!ok) break;
                 // ---- end of the piece (the PV of its last tile has finished): O / d of this row
                 if (!(ok = warp_wait(&sm.o_done, (J - 1) & 1))) break;
                 tc_fence_after();
-                uint32_t o[64];
-                tmem_ld32(tO, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
-                tmem_ld32(tO + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+                uint32_t raw[64];
+                tmem_ld32(tO, *reinterpret_cast<uint32_t(*)[32]>(&raw[0]));
+                tmem_ld32(tO + 32, *reinterpret_cast<uint32_t(*)[32]>(&raw[32]));
                 tc_wait_ld();
                 tc_fence_before();
-                const bool whole = seeded && tb == pc.tiles;
+                float o[64];
+#pragma unroll
+                for (int e = 0; e < 64; ++e) o[e] = __uint_as_float(raw[e]);
+                float scale_o = d > 0.f ? 1.f / d : 0.f, l2 = d > 0.f ? m + log2f(d) : kNegInf;
+                constexpr int kDims = kHeadDim / SPLIT;  // dims of the row that this thread finishes
+                int dim0 = 0;
+                if constexpr (SPLIT > 1) {
+                    // the copies' sums of a row, brought to one maximum, are added up: each thread gives the dims that it
+                    // does not finish to the thread of the same row in another copy
+                    const int t0 = tid - 128;
+                    sm.md[t0] = make_float2(m, d);
+                    mbar_arrive(&sm.exchange);
+                    if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
+                    float M = m, D = 0.f;
+#pragma unroll
+                    for (int c = 0; c < SPLIT; ++c) M = fmaxf(M, sm.md[c * kBlock + r].x);
+#pragma unroll
+                    for (int c = 0; c < SPLIT; ++c) {
+                        const float2 x = sm.md[c * kBlock + r];
+                        D += x.x == kNegInf ? 0.f : x.y * fast_exp2(x.x - M);
+                    }
+                    scale_o = (m == kNegInf || !(D > 0.f)) ? 0.f : fast_exp2(m - M) / D;
+                    // (all mass on nothing: a sink of -inf and no key)
+                    l2 = D > 0.f ? M + log2f(D) : kNegInf;
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) o[e] *= scale_o;
+                    scale_o = 1.f;
+                    // the piece's Q slot is free (its scores are done) and takes the first exchange
+                    float(*give)[kBM] = reinterpret_cast<float(*)[kBM]>(sm.q[p & 1]);
+                    const bool upper = copy & 1;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) give[e][t0] = upper ? o[e] : o[32 + e];
+                    mbar_arrive(&sm.exchange);
+                    if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = (upper ? o[32 + e] : o[e]) + give[e][t0 ^ kBlock];
+                    dim0 = upper ? 32 : 0;
+                    fence_proxy_async_smem();  // before a copy of query rows may land there
+                    mbar_arrive(&sm.q_empty[p & 1]);
+                    if constexpr (SPLIT == 4) {
+                        const bool upper2 = copy & 2;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) sm.half[e][t0] = upper2 ? o[e] : o[16 + e];
+                        mbar_arrive(&sm.exchange);
+                        if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = (upper2 ? o[16 + e] : o[e]) + sm.half[e][t0 ^ (2 * kBlock)];
+                        dim0 += upper2 ? 16 : 0;
+                    }
+                    ++p;
+                }
+                const bool starts = ta == 0, whole = starts && tb == pc.tiles;
                 const int seg = pc.b * Hkv + pc.g;
-                if (seeded && !whole) {
+                if (starts && !whole) {
                     long long c_first = 0;
                     int pieces = 0;
                     segment_pieces(pc.seg_start, pc.tiles, C, U, c_first, pieces);
                     head = make_int2(seg, pieces);
                 }
                 if (live) {
-                    const float inv = d > 0.f ? 1.f / d : 0.f;
-                    const float l2 = d > 0.f ? m + log2f(d) : kNegInf;
                     if (whole) {
                         const long long row = ((long long)pc.b * K + i) * a.Hq + pc.g * G + h;
-                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kHeadDim);
+                        uint4* dst = reinterpret_cast<uint4*>(a.out + row * kHeadDim + dim0);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < kDims / 8; ++e) {
                             uint4 w;
-                            w.x = pack_bf16(__uint_as_float(o[8 * e + 0]) * inv, __uint_as_float(o[8 * e + 1]) * inv);
-                            w.y = pack_bf16(__uint_as_float(o[8 * e + 2]) * inv, __uint_as_float(o[8 * e + 3]) * inv);
-                            w.z = pack_bf16(__uint_as_float(o[8 * e + 4]) * inv, __uint_as_float(o[8 * e + 5]) * inv);
-                            w.w = pack_bf16(__uint_as_float(o[8 * e + 6]) * inv, __uint_as_float(o[8 * e + 7]) * inv);
+                            w.x = pack_bf16(o[8 * e + 0] * scale_o, o[8 * e + 1] * scale_o);
+                            w.y = pack_bf16(o[8 * e + 2] * scale_o, o[8 * e + 3] * scale_o);
+                            w.z = pack_bf16(o[8 * e + 4] * scale_o, o[8 * e + 5] * scale_o);
+                            w.w = pack_bf16(o[8 * e + 6] * scale_o, o[8 * e + 7] * scale_o);
                             dst[e] = w;
                         }
-                        if (a.lse) a.lse[row] = l2 * kLn2;
+                        if (a.lse && copy == 0) a.lse[row] = l2 * kLn2;
                     } else {
                         const long long slot = cta + seg;  // partial slot of this piece
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * R + r) * kHeadDim);
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + (slot * R + r) * kHeadDim + dim0);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            dst[e] = make_float4(__uint_as_float(o[4 * e + 0]) * inv, __uint_as_float(o[4 * e + 1]) * inv,
-                                                 __uint_as_float(o[4 * e + 2]) * inv, __uint_as_float(o[4 * e + 3]) * inv);
-                        a.part_lse[slot * R + r] = l2;
+                        for (int e = 0; e < kDims / 4; ++e)
+                            dst[e] = make_float4(o[4 * e + 0] * scale_o, o[4 * e + 1] * scale_o, o[4 * e + 2] * scale_o,
+                                                 o[4 * e + 3] * scale_o);
+                        if (copy == 0) a.part_lse[slot * R + r] = l2;
                     }
                 }
             }
@@ -702,24 +806,32 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 }  // namespace
 
+// The kernel for R query rows: as many copies of them as the tile's 128 rows hold, so that all four softmax warps work.
+using BeamsKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const BeamsArgs);
+static BeamsKernel beams_kernel(int R, int* split) {
+    *split = R <= 32 ? 4 : (R <= 64 ? 2 : 1);
+    return R <= 32 ? decode_beams_kernel<4> : (R <= 64 ? decode_beams_kernel<2> : decode_beams_kernel<1>);
+}
+
 // CTAs of the attention kernel that fit on one SM, from its registers, its shared memory (with the per-block
 // reservation) and its tensor memory (512 columns per SM, kTmemCols per CTA); the runtime's occupancy query
 // reports one for a kernel that allocates tensor memory, while the hardware keeps two resident.
-static cudaError_t beams_occupancy(int* per_sm, int* sms) {
-    static thread_local int cached[64] = {};
-    int dev = 0;
+static cudaError_t beams_occupancy(int R, int* per_sm, int* sms) {
+    static thread_local int cached[64][5] = {};
+    int dev = 0, split = 1;
+    const BeamsKernel kernel = beams_kernel(R, &split);
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    if (dev < 64 && cached[dev] > 0) {
-        *per_sm = cached[dev];
+    if (dev < 64 && cached[dev][split] > 0) {
+        *per_sm = cached[dev][split];
         return cudaSuccess;
     }
     const size_t smem = 1024 + sizeof(Smem);
-    e = cudaFuncSetAttribute(decode_beams_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, decode_beams_kernel)) != cudaSuccess) return e;
+    if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return e;
     int smem_sm = 0, reserved = 0, regs_sm = 0;
     if ((e = cudaDeviceGetAttribute(&smem_sm, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev)) != cudaSuccess ||
         (e = cudaDeviceGetAttribute(&reserved, cudaDevAttrReservedSharedMemoryPerBlock, dev)) != cudaSuccess ||
@@ -732,7 +844,7 @@ static cudaError_t beams_occupancy(int* per_sm, int* sms) {
     n = n < by_smem ? n : by_smem;
     n = n < by_regs ? n : by_regs;
     if (n < 1) return cudaErrorInvalidConfiguration;
-    if (dev < 64) cached[dev] = n;
+    if (dev < 64) cached[dev][split] = n;
     *per_sm = n;
     return cudaSuccess;
 }
@@ -740,7 +852,7 @@ static cudaError_t beams_occupancy(int* per_sm, int* sms) {
 cudaError_t beams_plan(int N, int K, int Hq, int Hkv, int max_pages, int num_workers, BeamsPlan* plan) {
     const size_t R = (size_t)K * (Hq / Hkv);
     int per_sm = 0, sms = 0;
-    const cudaError_t e = beams_occupancy(&per_sm, &sms);
+    const cudaError_t e = beams_occupancy((int)R, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
     plan->tc_grid = num_workers > 0 ? num_workers : (long long)sms * per_sm;
@@ -757,8 +869,8 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
                                 const CUtensorMap& tv, bool may_split, cudaStream_t stream) {
     if (args.N == 0) return cudaSuccess;
     if (args.tc_grid > 0x7fffffffll || args.tc_grid < 1) return cudaErrorInvalidConfiguration;
-    int per_sm = 0, sms = 0;  // also sets the kernel's shared-memory limit
-    cudaError_t e = beams_occupancy(&per_sm, &sms);
+    int per_sm = 0, sms = 0, split = 1;  // the call also sets the kernel's shared-memory limit
+    cudaError_t e = beams_occupancy(args.R, &per_sm, &sms);
     if (e != cudaSuccess) return e;
     BeamsArgs a = args;
     if (!may_split) a.merge_list = nullptr;
@@ -785,7 +897,7 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = 1024 + sizeof(Smem);
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, decode_beams_kernel, tq, tk, tv, a);
+    e = cudaLaunchKernelEx(&cfg, beams_kernel(a.R, &split), tq, tk, tv, a);
     if (e != cudaSuccess || !may_split) return e;
     SplitMergeArgs m;
     m.part_o = a.part_o;
