@@ -6,8 +6,8 @@
 // between rows.  Softmax over a row's keys can be summed in any order and in any pieces, so the pages of a group
 // are taken not row by row but once each: every distinct (column, page) with the set of rows that hold it.
 //
-// GB300 design.  beams_plan_kernel lists each group's distinct pages (8 columns' worth of a K x max_pages table
-// to the microsecond: latency); decode_beams_kernel, its programmatic dependent, streams them.  The R = K x G
+// GB300 design.  beams_plan_kernel lists each group's distinct pages (its time is
+// latency: a few dependent loads); decode_beams_kernel, its programmatic dependent, streams them.  The R = K x G
 // query rows of one (group n, KV head g) -- row r = k * G + h is row k's query head g * G + h -- form ONE tcgen05
 // tile (R <= 128, padded to the MMA's 128 rows), so a page is read once for all rows and every product runs on
 // the tensor core; a row's keys are masked by the page's row set and the row's own length.
@@ -21,9 +21,15 @@
 //   warp 2      issues O += P_j V_j (P read from TMEM; the first tile of a piece starts O afresh).
 //   warps 4-7   softmax, thread r = row r (only the warps that hold rows work); at a piece's end they read O and
 //               write the rows (or fp32 partials).
+// A row fills a quarter or half of the tile's rows where R allows it: the query rows are then loaded two or four
+// times, every copy takes its half or quarter of a tile's keys (the other keys' weights stay zero, so the products
+// keep their form) and a state of its own, and the copies' states are put together at a piece's end.  All four
+// softmax warps work then: with 8 rows of 8 heads over one long prompt the call takes 186 us instead of 202.
 // The piece with a segment's first tile is seeded with the sink.  The pieces of a segment split between CTAs
 // write fp32 partials; the CTA holding the segment's first piece lists it, and the split-merge kernel, launched
-// right behind this one as a programmatic dependent, combines them.  Every wait is bounded.
+// right behind this one as a programmatic dependent, combines them (merging in the CTA that finishes a segment's last
+// piece takes longer: the fences that order its partials before the count wait for the copies in flight; 76 us against
+// 57 for 32 groups of 8 rows).  Every wait is bounded.
 #include "args_beams.h"
 #include "args_merge.h"
 #include "ptx.cuh"
@@ -46,16 +52,16 @@ constexpr int kKStages = 2, kVStages = 2;
 constexpr int kPagesPerTile = kBN / kPageSize;  // 8
 constexpr int kMinTiles = kBeamsMinTiles;  // automatic mode: never cut shares finer than this
 
-constexpr int kPlanThreads = 256;
-
 // Lists the distinct pages of group blockIdx.x / ctas, by column and, within one, by the first row that holds
-// them.  Each of the group's `ctas` CTAs (a cluster) takes a contiguous run of columns, a thread one column at a
-// time; with more than one CTA the columns are counted first, so that each knows where its entries start.
+// them; the group's CTAs are a cluster.  A thread takes one column of all rows, every load issued before any is looked
+// at, and keeps the page ids while the counts of the CTA's threads and of the cluster's CTAs say where its entries
+// go.  A column's pages are found one after another (mostly there is one), which keeps the code short: the kernel runs
+// for a few microseconds and would spend them fetching instructions.
 template <int KMAX>
-__global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArgs a) {
+__global__ void __launch_bounds__(KMAX <= 8 ? 1024 : (KMAX == 16 ? 512 : 256)) beams_plan_kernel(const BeamsArgs a) {
     __shared__ int len[kBeamsMaxBeams];
-    __shared__ int red[kPlanThreads / 32];
-    __shared__ int counted;
+    __shared__ int red[32];
+    __shared__ int counted[2];
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -72,38 +78,38 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
         longest = max(longest, len[k]);
         shortest = min(shortest, len[k]);
     }
-    const int cols = (longest + kPageSize - 1) / kPageSize;
-    const int per = (cols + ctas - 1) / ctas, c0 = min(cols, rank * per), c1 = min(cols, c0 + per);
+    const int cols = (longest + kPageSize - 1) / kPageSize, threads = (int)blockDim.x, step = ctas * threads;
     const int* table = a.page_table + (long long)n * K * a.max_pages;
-
-    int id[KMAX];       // the column's page of each row, -1 where it has none
-    unsigned set[KMAX]; // the rows that hold the same page, for the first of them; else 0
+    PageEntry* out = a.entries + (long long)n * K * a.max_pages;
     bool bad = false;
-    auto column = [&](int c) {
-        auto holds = [&](int k) { return k < K && c < c1 && c * kPageSize < len[k]; };
+    int at = 0;
+    for (int q = 0, base = 0; base < cols; base += step, ++q) {
+        const int c = base + rank * threads + tid;
+        auto holds = [&](int k) { return k < K && c < cols && c * kPageSize < len[k]; };
+        int id[KMAX];  // the column's page of each row, -1 where it has none
 #pragma unroll
-        for (int k = 0; k < KMAX; ++k)  // every row's load before any is looked at
-            id[k] = holds(k) ? __ldcg(&table[(long long)k * a.max_pages + c]) : -1;
-        int distinct = 0;
+        for (int k = 0; k < KMAX; ++k) id[k] = holds(k) ? __ldcg(&table[(long long)k * a.max_pages + c]) : -1;
+        unsigned held = 0;  // the rows that hold a page of the column
 #pragma unroll
         for (int k = 0; k < KMAX; ++k) {
-            if (id[k] < 0 || id[k] >= a.num_pages) {
-                bad |= holds(k);
-                id[k] = -1;
-            }
+            if (id[k] >= 0 && id[k] < a.num_pages) held |= 1u << k;
+            else bad |= holds(k);
         }
+        // the first of the rows `left`'s page, and which of them hold it
+        auto first_page = [&](unsigned left, int& page) {
+            const int first = __ffs(left) - 1;
+            page = id[0];
 #pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
+            for (int k = 1; k < KMAX; ++k) page = k == first ? id[k] : page;
             unsigned same = 0;
 #pragma unroll
-            for (int j = 0; j < KMAX; ++j) same |= (id[j] == id[k]) ? 1u << j : 0u;
-            set[k] = (id[k] >= 0 && __ffs(same) - 1 == k) ? same : 0u;
-            distinct += set[k] != 0u;
-        }
-        return distinct;
-    };
-    auto block_sum = [&](int v, int& total) {  // exclusive prefix of v over the CTA's threads
-        int incl = v;
+            for (int k = 0; k < KMAX; ++k) same |= id[k] == page ? 1u << k : 0u;
+            return same & left;
+        };
+        int mine = 0, page;
+#pragma unroll 1
+        for (unsigned left = held; left; ++mine) left &= ~first_page(left, page);
+        int incl = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -112,44 +118,36 @@ __global__ void __launch_bounds__(kPlanThreads) beams_plan_kernel(const BeamsArg
         __syncthreads();
         if (lane == 31) red[warp] = incl;
         __syncthreads();
-        int before = 0;
-        total = 0;
-#pragma unroll
-        for (int w = 0; w < kPlanThreads / 32; ++w) {
-            before += w < warp ? red[w] : 0;
-            total += red[w];
+        const int w = lane < threads / 32 ? red[lane] : 0;
+        int total = __reduce_add_sync(0xffffffffu, w);
+        int to = at + incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+        if (ctas > 1) {
+            if (tid == 0) counted[q & 1] = total;
+            cluster.sync();
+            total = 0;
+            for (int i = 0; i < ctas; ++i) {
+                const int there = cluster.map_shared_rank(counted, i)[q & 1];
+                to += i < rank ? there : 0;
+                total += there;
+            }
         }
-        return before + incl - v;
-    };
-
-    int at = 0, total;
-    if (ctas > 1) {
-        int mine = 0;
-        for (int c = c0 + tid; c < c1; c += kPlanThreads) mine += column(c);
-        (void)block_sum(mine, total);
-        if (tid == 0) counted = total;
-        cluster.sync();
-        for (int i = 0; i < rank; ++i) at += *cluster.map_shared_rank(&counted, i);
-        cluster.sync();  // no CTA ends while another reads its count
-    }
-    PageEntry* out = a.entries + (long long)n * K * a.max_pages;
-    for (int base = c0; base < c1; base += kPlanThreads) {
-        const int c = base + tid, distinct = column(c);
-        int to = at + block_sum(distinct, total);
-#pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
-            if (!set[k]) continue;
-            int slots = 0;
-#pragma unroll
-            for (int j = 0; j < KMAX; ++j)
-                if ((set[k] >> j) & 1u) slots = max(slots, min(kPageSize, len[j] - c * kPageSize));
-            const bool all = __popc(set[k]) == K && shortest >= (c + 1) * kPageSize;
-            *reinterpret_cast<int4*>(out + to++) = make_int4(id[k], c, (int)set[k], slots | (all ? kAllSee : 0));
+#pragma unroll 1
+        for (unsigned left = held; left;) {
+            const unsigned same = first_page(left, page);
+            left &= ~same;
+            int slots = kPageSize;
+            if (shortest < (c + 1) * kPageSize) {  // the longest of its rows fills how much of it
+                slots = 0;
+                for (unsigned m = same; m; m &= m - 1) slots = max(slots, min(kPageSize, len[__ffs(m) - 1] - c * kPageSize));
+            }
+            const bool all = __popc(same) == K && shortest >= (c + 1) * kPageSize;
+            *reinterpret_cast<int4*>(out + to++) = make_int4(page, c, (int)same, slots | (all ? kAllSee : 0));
         }
         at += total;
     }
     if (bad) atomicOr(a.err, kErrBadPage);
-    if (rank == ctas - 1 && tid == 0) a.counts[n] = at;
+    if (rank == 0 && tid == 0) a.counts[n] = at;
+    if (ctas > 1) cluster.sync();  // no CTA ends while another reads its count
 }
 
 // What the plan kernel wrote is read through L2 (ld.cg): this kernel may be resident before it has been written.
@@ -219,10 +217,20 @@ struct __align__(1024) Smem {
     long long found[4];  // share start: group, its first unit, its tiles, flag
     Walk walk[4];        // the softmax warps' walkers (kept out of their registers)
     Piece piece[4];      // ... and their current pieces
-    int4 entry[4][2][kPagesPerTile];  // ... and their pages' entries, this tile's and the next one's
+    int4 entry[4][2][kPagesPerTile];  // the softmax warps' page entries, this tile's and the next one's
     float2 md[kBM];                   // SPLIT > 1: running maximum and normaliser of every thread at a piece's end
     float half[16][kBM];              // SPLIT = 4: the second exchange of partial sums
 };
+
+// The next piece of softmax warp `w`'s walk, found by its first lane; null at the end of the share.
+__device__ __forceinline__ const Piece* next_piece(const BeamsArgs& a, Smem& sm, int w, int lane) {
+    int has = 0;
+    __syncwarp();  // every lane is done with the previous piece
+    if (lane == 0) has = sm.walk[w].next(a, sm.piece[w]) ? 1 : 0;
+    has = __shfl_sync(0xffffffffu, has, 0);
+    __syncwarp();
+    return has ? &sm.piece[w] : nullptr;
+}
 
 // cp.async of 16 bytes through L2, and the wait for all of a thread's.
 __device__ __forceinline__ void copy16_async(void* smem, const void* gmem) {
@@ -400,6 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.seg_start = sm.found[1] + (long long)walk.g * walk.tiles;
     walk.x = x0;
     walk.x1 = x1;
+    if (tid < 4) sm.walk[tid] = walk;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -563,15 +572,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             int J = 0, p = 0, ex = 0;  // tiles, pieces, phases of the exchange barrier
             bool ok = true;
             const int sw = warp - 4;
-            if (lane == 0) sm.walk[sw] = walk;
-            __syncwarp();
             while (ok) {
-                int has = 0;
-                __syncwarp();  // every lane is done with the previous piece
-                if (lane == 0) has = sm.walk[sw].next(a, sm.piece[sw]) ? 1 : 0;
-                if (!__shfl_sync(0xffffffffu, has, 0)) break;
-                __syncwarp();
-                const Piece& pc = sm.piece[sw];
+                const Piece* next = next_piece(a, sm, sw, lane);
+                if (!next) break;
+                const Piece& pc = *next;
                 const int ta = pc.ta, tb = pc.tb, pages = pc.pages;
                 const PageEntry* entries = a.entries + (long long)pc.b * K * a.max_pages;
                 // the entries of a tile's pages are copied to shared memory one tile ahead (in registers they would not fit
@@ -874,8 +878,10 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
     if (e != cudaSuccess) return e;
     BeamsArgs a = args;
     if (!may_split) a.merge_list = nullptr;
-    // one CTA lists a group of up to four steps of columns, a cluster of eight a longer one
-    const int ctas = a.max_pages <= 4 * kPlanThreads ? 1 : 8;
+    // a thread per column: one CTA while its threads are enough, else a cluster of eight
+    const int most = a.K <= 8 ? 1024 : (a.K <= 16 ? 512 : 256);
+    const int ctas = a.max_pages <= most ? 1 : 8;
+    const int per = (a.max_pages + ctas - 1) / ctas, threads = per >= most ? most : (per + 31) / 32 * 32;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -884,7 +890,7 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.N * ctas));
-    cfg.blockDim = dim3(kPlanThreads);
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
