@@ -214,7 +214,7 @@ struct __align__(1024) Smem {
     uint64_t s_full, s_free, p_full, o_done, mma_done, exchange;
     uint32_t tmem_base;
     long long red[8];    // block reductions
-    long long found[4];  // share start: group, its first unit, its tiles, flag
+    long long found[4];  // share start: group, its first unit, its pages, flag
     Walk walk[4];        // the softmax warps' walkers (kept out of their registers)
     Piece piece[4];      // ... and their current pieces
     int4 entry[4][2][kPagesPerTile];  // the softmax warps' page entries, this tile's and the next one's
@@ -304,12 +304,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     // group holding this share's first unit (one pass when the batch fits the CTA's threads)
     if (tid == 0) sm.found[3] = 0;
     long long U = 0, base = 0, lo = 0, cnt = 0;
+    int pages_here = 0;
     for (int p0 = 0; p0 < B; p0 += kThreads) {
         const int i = p0 + tid;
-        int ti = 0;
-        if (i < B) {
-            ti = tiles_of(count_of(a, i));
-        }
+        const int n_pages = i < B ? count_of(a, i) : 0, ti = tiles_of(n_pages);
         const long long c = (long long)ti * Hkv;
         long long incl = c;
 #pragma unroll
@@ -329,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (B <= kThreads) {  // one pass: this thread's request and its units stay in registers
             lo = woff + incl - c;
             cnt = c;
+            pages_here = n_pages;
         }
         U = base + total;
         base = U;
@@ -361,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (cnt > 0 && x0 >= lo && x0 < lo + cnt) {
             sm.found[0] = tid;
             sm.found[1] = lo;
-            sm.found[2] = cnt / Hkv;
+            sm.found[2] = pages_here;
         }
         __syncthreads();
     } else {
@@ -369,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         base = 0;
         for (int p0 = 0; p0 < B; p0 += kThreads) {
             const int i = p0 + tid;
-            const int ti = i < B ? tiles_of(count_of(a, i)) : 0;
+            const int n_pages = i < B ? count_of(a, i) : 0, ti = tiles_of(n_pages);
             const long long c = (long long)ti * Hkv;
             long long incl = c;
 #pragma unroll
@@ -390,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (c > 0 && x0 >= l0 && x0 < l0 + c) {
                 sm.found[0] = i;
                 sm.found[1] = l0;
-                sm.found[2] = ti;
+                sm.found[2] = n_pages;
                 sm.found[3] = 1;
             }
             base += total;
@@ -402,8 +401,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.B = B;
     walk.Hkv = Hkv;
     walk.b = (int)sm.found[0];
-    walk.tiles = (int)sm.found[2];
-    walk.pages = count_of(a, walk.b);
+    walk.pages = (int)sm.found[2];
+    walk.tiles = tiles_of(walk.pages);
     walk.g = (int)((x0 - sm.found[1]) / walk.tiles);
     walk.seg_start = sm.found[1] + (long long)walk.g * walk.tiles;
     walk.x = x0;
@@ -416,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (warp < 4) {
         // 128 x kFew + 128 x kMany = 256 x 128, the launch's registers: a thread's scores of a whole tile want many
-        constexpr int kFew = SPLIT > 1 ? 96 : 80;
+        constexpr int kFew = SPLIT > 1 ? 96 : 64;
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFew));
         if (warp == 0 || warp == 3) {
             // ------------------------------------------------------------ TMA producers
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             (void)warp_wait(&sm.mma_done, 0);
         }
     } else {
-        constexpr int kMany = SPLIT > 1 ? 160 : 176;
+        constexpr int kMany = SPLIT > 1 ? 160 : 192;
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMany));
         const int copy = (tid - 128) / kBlock, r = (tid - 128) % kBlock;  // copy of the query rows, row
         const bool live = r < R;
