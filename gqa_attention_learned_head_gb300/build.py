@@ -75,8 +75,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> Path:
     return LIB
 
 
-# Host code with the most validation logic: the C ABI layer and the no-allocation entry point.
-SANITIZED_SOURCES = ("api.cu", "decode_noalloc.cu")
+# Host code with the most validation logic: the C ABI layers and the no-allocation entry point.
+SANITIZED_SOURCES = ("api.cu", "api_beam.cu", "decode_noalloc.cu")
 SAN_BUILD = PKG / "_build_san"
 SAN_LIB = SAN_BUILD / "libsinkattn.so"
 SAN_FLAGS = ["-Xcompiler", "-fsanitize=address", "-Xcompiler", "-fsanitize=undefined", "-Xcompiler", "-fno-omit-frame-pointer",

@@ -50,7 +50,7 @@ sinkattn_status_t check_move_dims(const sinkattn_move_dims_t* d, bool compact) {
     if (compact && (d->max_accepted > kMaxAccepted || (long long)d->max_pages * kPageSize >= (1ll << 31)))
         return SINKATTN_ERR_UNSUPPORTED;
     // the kernel's units (warps) and a layer's rows
-    if ((long long)d->num_pages * d->num_kv_heads * kPageSize >= (1ll << 31) ||
+    if ((long long)d->num_pages * d->num_kv_heads >= (1ll << 31) / kPageSize ||
         (double)d->num_layers * d->num_rows * d->num_kv_heads > 8e9)
         return SINKATTN_ERR_UNSUPPORTED;
     return SINKATTN_OK;
@@ -65,7 +65,7 @@ sinkattn_status_t check_beams_dims(const sinkattn_beams_dims_t* d) {
         (long long)d->num_beams * (d->num_q_heads / d->num_kv_heads) > kBeamsMaxRows)
         return SINKATTN_ERR_UNSUPPORTED;
     // TMA row coordinates are 32-bit, and so are a row's tokens and a group's page entries
-    if ((long long)d->num_pages * d->num_kv_heads * kPageSize >= (1ll << 31) ||
+    if ((long long)d->num_pages * d->num_kv_heads >= (1ll << 31) / kPageSize ||
         (long long)d->max_pages * (d->num_beams > kPageSize ? d->num_beams : kPageSize) >= (1ll << 31))
         return SINKATTN_ERR_UNSUPPORTED;
     return SINKATTN_OK;

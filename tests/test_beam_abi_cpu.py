@@ -106,3 +106,57 @@ def test_decode_beams_dims(S):
                dict(num_pages=1 << 27), dict(max_pages=1 << 27)):
         assert call(**kw) == S.ERR_UNSUPPORTED, kw
     assert call(num_groups=0) == S.OK
+
+
+SANITIZED_CHILD = r"""
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+from gqa_attention_learned_head_gb300 import abi
+lib = abi.declare(ctypes.CDLL(sys.argv[2]))
+big = 2 ** 31 - 1
+n = 0
+for d in (abi.BeamDims(-1, 4, 10, 4, 1, 0, 10), abi.BeamDims(1, 33, 10, 4, 1, 0, 10), abi.BeamDims(big, 32, big, 64, 2, 0, 2 ** 62),
+          abi.BeamDims(1, 4, 10, 4, 7, 0, 10), abi.BeamDims(1, 4, 10, 65, 1, 0, 10), abi.BeamDims(65535, 32, 2 ** 30, 64, 0, 0, 2 ** 40)):
+    assert lib.sinkattn_beam_select(*[None] * 6, ctypes.byref(d), None, 0, None) != 0
+    assert lib.sinkattn_beam_select_workspace_size(ctypes.byref(d)) == 0
+    n += 1
+for d in (abi.ForkDims(big, 1, 1, 1, 16, 0), abi.ForkDims(1, big, 1, 1, 16, 0), abi.ForkDims(1, 1, big, 1, 16, 0),
+          abi.ForkDims(1, 1, 1, big, 16, 0), abi.ForkDims(1, 1, 1, 1, 16, -big), abi.ForkDims(1, 1, 1, 1, 8, 0)):
+    assert lib.sinkattn_pages_fork(*[None] * 10, ctypes.byref(d), None, 0, None) != 0
+    assert lib.sinkattn_pages_fork_workspace_size(ctypes.byref(d)) == 0
+    n += 1
+assert lib.sinkattn_pages_fork_workspace_size(ctypes.byref(abi.ForkDims(1 << 20, 1 << 20, 1 << 30, (1 << 27) - 1, 16, big))) > 0
+for d in (abi.MoveDims(big, big, big, 64, 16, big, big, 16), abi.MoveDims(0, 1, 1, 64, 16, 1, 1, 1), abi.MoveDims(big, 1 << 20, 8, 64, 16, 1, 1, 1),
+          abi.MoveDims(1, 1, big, 64, 16, big, 1, 1)):
+    assert lib.sinkattn_kv_copy(None, None, None, ctypes.byref(d), None) != 0
+    assert lib.sinkattn_kv_compact(*[None] * 6, ctypes.byref(d), None) != 0
+    n += 1
+for d in (abi.BeamsDims(big, 32, big, 1, 64, 16, big, big, big), abi.BeamsDims(1, 32, 8, 1, 64, 16, 1, 1, 0),
+          abi.BeamsDims(1, 1, 8, 1, 64, 16, 1, 1 << 27, 0), abi.BeamsDims(1, 1, 0, 1, 64, 16, 1, 1, 0)):
+    assert lib.sinkattn_decode_beams(*[None] * 6, 0.125, None, None, ctypes.byref(d), None, 0, None) != 0
+    assert lib.sinkattn_decode_beams_workspace_size(ctypes.byref(d)) == 0
+    n += 1
+print("ok", n)
+"""
+
+
+def test_beam_validation_under_sanitizers():
+    """The host code of the beam step's entry points, built with AddressSanitizer and UndefinedBehaviorSanitizer, refuses
+    dims at the ends of their types without a sanitizer report."""
+    import os
+    import subprocess
+    import sys
+    from pathlib import Path
+
+    from gqa_attention_learned_head_gb300 import build
+
+    asan = subprocess.run(["gcc", "-print-file-name=libasan.so"], capture_output=True, text=True).stdout.strip()
+    if not asan or not os.path.isabs(asan) or not os.path.exists(asan):
+        pytest.skip("the AddressSanitizer runtime is not installed")
+    lib = build.build_sanitized()
+    env = dict(os.environ, LD_PRELOAD=asan, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
+               UBSAN_OPTIONS="halt_on_error=1:print_stacktrace=1")
+    r = subprocess.run([sys.executable, "-c", SANITIZED_CHILD, str(Path(__file__).resolve().parents[1]), str(lib)], env=env,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-2000:] + r.stderr[-4000:]
+    assert "AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-4000:]

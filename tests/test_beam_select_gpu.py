@@ -216,6 +216,26 @@ def test_bad_values_are_reported_and_their_beam_left_out(S, where):
     assert S.sinkattn_get_error() == 0
 
 
+@pytest.mark.parametrize("fill", ["random", "equal", "one quad"])
+def test_largest_shares(S, fill):
+    """Rows of more than one full share of 262144 tokens, the most picks: the lists at their capacity."""
+    V, M = 2 * 262144 + 77, 64
+    z, c = make(1, 2, V, torch.float32, seed=21)
+    if fill == "equal":
+        z[:] = 0.25
+    elif fill == "one quad":  # the best tokens of all of a quad of threads' groups: two groups of every 128
+        z = z.view(-1)
+        lead = torch.arange(2 * V, device="cuda") % V % 4096 < 64
+        z = torch.where(lead, z + 50, z).view(1, 2, V)
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    if fill == "equal":
+        best = 0 if float(c[0, 0]) >= float(c[0, 1]) else 1
+        assert torch.equal(got[2].cpu(), torch.arange(M, dtype=torch.int32)[None]) and (got[1] == best).all()
+    else:
+        check(got, reference(z, c, M))
+
+
 def test_groups_and_empty_call(S):
     z, c = make(1, 2, 100, torch.float32, seed=1)
     s, p, t = S.sinkattn_beam_select(z[:0], c[:0], 4)

@@ -148,6 +148,13 @@ def test_many_groups(S):
     check(S, *make(4, 2, lens, seed=37), what="700 groups")
 
 
+def test_most_groups(S):
+    """The largest batch, a row or two each."""
+    rng = random.Random(2)
+    lens = [[rng.randint(0, 20)] for _ in range(32768)]
+    check(S, *make(2, 1, lens, seed=44, garbage=False), what="32768 groups")
+
+
 def test_equals_decode_on_the_rows(S):
     q, k, v, table, lens, sinks = (t.cuda() for t in make(64, 8, [[1000] * 8, [333] * 8], seed=38, garbage=False))
     out, lse = S.sinkattn_decode_beams(q, k, v, table, lens, sinks, 0.125)

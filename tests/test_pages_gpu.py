@@ -191,6 +191,37 @@ def test_large_pool_and_table(S):
     same(got, fork_reference(table, held, parents, refs, keep, room), mp)
 
 
+def test_no_pool(S):
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    out = S.sinkattn_pages_fork(torch.empty(0, 2, dtype=torch.int32, device="cuda"), none, ints([-1]), none, room_lens=ints([5]))
+    assert S.sinkattn_get_error() == S.ERR_NO_PAGES and out[0].tolist() == [[-1, -1]] and out[1].tolist() == [0]
+
+
+@pytest.mark.parametrize("mp", [3, 4, 6, 9])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_row_lengths_and_alignments(S, mp, shift):
+    """Rows of every length modulo 16 bytes, tables and counts that start at any entry."""
+    rng = random.Random(mp)
+    table, held, refs = random_state(rng, 20, mp, 200)
+    parents = [rng.randint(-1, 19) for _ in range(30)]
+    room = [min(mp * PS, (held[p] if p >= 0 else 0) + rng.randint(0, 20)) for p in parents]
+    keep = [held[p] if p >= 0 else 0 for p in parents]
+
+    def off(x):  # the same values, starting `shift` entries into a buffer
+        t = torch.as_tensor(x, dtype=torch.int32)
+        buf = torch.zeros(t.numel() + shift, dtype=torch.int32, device="cuda")
+        buf[shift:] = t.reshape(-1).cuda()
+        return buf[shift:].view(t.shape)
+
+    t = torch.zeros(20, mp, dtype=torch.int32)
+    for i, row in enumerate(table):
+        t[i, :len(row)] = torch.tensor(row, dtype=torch.int32)
+    got = S.sinkattn_pages_fork(off(t), off(held), off(parents), off(refs), off(keep), off(room),
+                                out_table=off(torch.zeros(30, mp)), out_refs=off(torch.zeros(200)))
+    assert S.sinkattn_get_error() == 0
+    same(got, fork_reference(table, held, parents, refs, keep, room), mp)
+
+
 def test_short_of_pages(S):
     table, held, refs = [[0, 1]], [20], [1, 1, 0, 0]
     got = call(S, table, 8, held, [0, -1], refs, [20, 0], [20, 33])  # three new pages, two free
