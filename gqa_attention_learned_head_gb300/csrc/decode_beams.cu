@@ -52,75 +52,61 @@ constexpr int kKStages = 2, kVStages = 2;
 constexpr int kPagesPerTile = kBN / kPageSize;  // 8
 constexpr int kMinTiles = kBeamsMinTiles;  // automatic mode: never cut shares finer than this
 
+constexpr int kPlanSteps = 8;  // columns of a lane in one pass
+
 // Lists the distinct pages of group blockIdx.x / ctas, by column and, within one, by the first row that holds
-// them; the group's CTAs are a cluster.  A thread takes one column of all rows, every load issued before any is looked
-// at, and keeps the page ids while the counts of the CTA's threads and of the cluster's CTAs say where its entries
-// go.  A column's pages are found one after another (mostly there is one), which keeps the code short: the kernel runs
-// for a few microseconds and would spend them fetching instructions.
-template <int KMAX>
-__global__ void __launch_bounds__(KMAX <= 8 ? 1024 : (KMAX == 16 ? 512 : 256)) beams_plan_kernel(const BeamsArgs a) {
+// them; the group's CTAs are a cluster.  LANES neighbouring lanes take a column, one row each, so that one match over
+// the warp finds every row's fellows, and a warp `steps` times 32 / LANES columns one after another, with all their
+// loads issued first; the counts of the CTA's warps and of the cluster's CTAs then say where its entries go.
+template <int LANES>
+__global__ void __launch_bounds__(1024) beams_plan_kernel(const BeamsArgs a, const int steps) {
     __shared__ int len[kBeamsMaxBeams];
     __shared__ int red[32];
     __shared__ int counted[2];
     cg::cluster_group cluster = cg::this_cluster();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, K = a.K, cap = a.max_pages * kPageSize;
+    constexpr int kCols = 32 / LANES;  // columns of a warp's step
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x / 32;
+    const int K = a.K, cap = a.max_pages * kPageSize, k = lane % LANES, sub = lane / LANES;
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), n = (int)(blockIdx.x / (unsigned)ctas);
-    if (tid < K) {
-        const int raw = __ldcg(&a.kv_lens[(long long)n * K + tid]);
-        if ((raw < 0 || raw > cap) && rank == 0) atomicOr(a.err, kErrBadLength);
-        len[tid] = clamp_len(raw, cap);
+    int mine = 0;  // this lane's row's cached tokens
+    if (k < K) {
+        const int raw = __ldcg(&a.kv_lens[(long long)n * K + k]);
+        if ((raw < 0 || raw > cap) && rank == 0 && warp == 0 && sub == 0) atomicOr(a.err, kErrBadLength);
+        mine = clamp_len(raw, cap);
     }
-    __syncthreads();
-    int longest = 0, shortest = cap;
-    for (int k = 0; k < K; ++k) {
-        longest = max(longest, len[k]);
-        shortest = min(shortest, len[k]);
-    }
-    const int cols = (longest + kPageSize - 1) / kPageSize, threads = (int)blockDim.x, step = ctas * threads;
-    const int* table = a.page_table + (long long)n * K * a.max_pages;
+    if (warp == 0 && sub == 0) len[k] = mine;
+    const int longest = __reduce_max_sync(0xffffffffu, mine), shortest = __reduce_min_sync(0xffffffffu, k < K ? mine : cap);
+    const int cols = (longest + kPageSize - 1) / kPageSize, held = (mine + kPageSize - 1) / kPageSize;  // held: by this row
+    const int* row = a.page_table + ((long long)n * K + (k < K ? k : 0)) * a.max_pages;
     PageEntry* out = a.entries + (long long)n * K * a.max_pages;
+    const unsigned fellows = LANES == 32 ? 0xffffffffu : ((1u << (LANES & 31)) - 1) << (sub * LANES);
+    const int per = steps * kCols;  // columns of a warp's pass
     bool bad = false;
     int at = 0;
-    for (int q = 0, base = 0; base < cols; base += step, ++q) {
-        const int c = base + rank * threads + tid;
-        auto holds = [&](int k) { return k < K && c < cols && c * kPageSize < len[k]; };
-        int id[KMAX];  // the column's page of each row, -1 where it has none
+    for (long long q = 0, base = 0; base < cols; base += (long long)ctas * warps * per, ++q) {
+        const long long c0 = base + (long long)(rank * warps + warp) * per + sub;
+        int id[kPlanSteps];
 #pragma unroll
-        for (int k = 0; k < KMAX; ++k) id[k] = holds(k) ? __ldcg(&table[(long long)k * a.max_pages + c]) : -1;
-        unsigned held = 0;  // the rows that hold a page of the column
+        for (int s = 0; s < kPlanSteps; ++s) id[s] = s < steps && c0 + s * kCols < held ? __ldcg(&row[c0 + s * kCols]) : -1;
+        unsigned same[kPlanSteps];  // the rows that hold this lane's page, for the first of them; else 0
+        int count = 0;
 #pragma unroll
-        for (int k = 0; k < KMAX; ++k) {
-            if (id[k] >= 0 && id[k] < a.num_pages) held |= 1u << k;
-            else bad |= holds(k);
-        }
-        // the first of the rows `left`'s page, and which of them hold it
-        auto first_page = [&](unsigned left, int& page) {
-            const int first = __ffs(left) - 1;
-            page = id[0];
-#pragma unroll
-            for (int k = 1; k < KMAX; ++k) page = k == first ? id[k] : page;
-            unsigned same = 0;
-#pragma unroll
-            for (int k = 0; k < KMAX; ++k) same |= id[k] == page ? 1u << k : 0u;
-            return same & left;
-        };
-        int mine = 0, page;
-#pragma unroll 1
-        for (unsigned left = held; left; ++mine) left &= ~first_page(left, page);
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+        for (int s = 0; s < kPlanSteps; ++s) {
+            same[s] = 0;
+            if (s >= steps) continue;
+            const bool there = id[s] >= 0 && id[s] < a.num_pages;
+            bad |= !there && c0 + s * kCols < held;
+            const unsigned all = __match_any_sync(0xffffffffu, there ? id[s] : ~lane) & fellows;
+            if (there && __ffs(all) - 1 == lane) same[s] = all;
+            count += __popc(__ballot_sync(0xffffffffu, same[s] != 0));
         }
         __syncthreads();
-        if (lane == 31) red[warp] = incl;
+        if (lane == 0) red[warp] = count;
         __syncthreads();
-        const int w = lane < threads / 32 ? red[lane] : 0;
-        int total = __reduce_add_sync(0xffffffffu, w);
-        int to = at + incl - mine + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+        const int w = lane < warps ? red[lane] : 0;
+        int total = __reduce_add_sync(0xffffffffu, w), to = at + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
         if (ctas > 1) {
             if (tid == 0) counted[q & 1] = total;
             cluster.sync();
@@ -131,17 +117,23 @@ __global__ void __launch_bounds__(KMAX <= 8 ? 1024 : (KMAX == 16 ? 512 : 256)) b
                 total += there;
             }
         }
-#pragma unroll 1
-        for (unsigned left = held; left;) {
-            const unsigned same = first_page(left, page);
-            left &= ~same;
-            int slots = kPageSize;
-            if (shortest < (c + 1) * kPageSize) {  // the longest of its rows fills how much of it
-                slots = 0;
-                for (unsigned m = same; m; m &= m - 1) slots = max(slots, min(kPageSize, len[__ffs(m) - 1] - c * kPageSize));
+#pragma unroll
+        for (int s = 0; s < kPlanSteps; ++s) {
+            if (s >= steps) continue;
+            const unsigned leaders = __ballot_sync(0xffffffffu, same[s] != 0);
+            if (same[s]) {
+                const int c = (int)c0 + s * kCols;
+                const unsigned rows = same[s] >> (sub * LANES);
+                int slots = kPageSize;
+                if (shortest < (c + 1) * kPageSize) {  // how much of it the longest of its rows fills
+                    slots = 0;
+                    for (unsigned m = rows; m; m &= m - 1) slots = max(slots, min(kPageSize, len[__ffs(m) - 1] - c * kPageSize));
+                }
+                const bool all = __popc(rows) == K && shortest >= (c + 1) * kPageSize;
+                *reinterpret_cast<int4*>(out + to + __popc(leaders & ((1u << lane) - 1))) =
+                    make_int4(id[s], c, (int)rows, slots | (all ? kAllSee : 0));
             }
-            const bool all = __popc(same) == K && shortest >= (c + 1) * kPageSize;
-            *reinterpret_cast<int4*>(out + to++) = make_int4(page, c, (int)same, slots | (all ? kAllSee : 0));
+            to += __popc(leaders);
         }
         at += total;
     }
@@ -877,10 +869,16 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
     if (e != cudaSuccess) return e;
     BeamsArgs a = args;
     if (!may_split) a.merge_list = nullptr;
-    // a thread per column: one CTA while its threads are enough, else a cluster of eight
-    const int most = a.K <= 8 ? 1024 : (a.K <= 16 ? 512 : 256);
-    const int ctas = a.max_pages <= most ? 1 : 8;
-    const int per = (a.max_pages + ctas - 1) / ctas, threads = per >= most ? most : (per + 31) / 32 * 32;
+    // the plan: as many lanes a column as rows, two columns a lane where a CTA's threads are enough, else up to
+    // kPlanSteps; clusters of up to eight CTAs, while all groups' CTAs find room on half of the SMs or the columns need them
+    const int lanes = a.K <= 4 ? 4 : (a.K <= 8 ? 8 : (a.K <= 16 ? 16 : 32));
+    const long long wanted = (long long)a.max_pages * lanes;
+    int ctas = 1;
+    while (ctas < 8 && wanted > 2048ll * ctas && ((long long)a.N * ctas * 4 <= sms || wanted > 1024ll * kPlanSteps * ctas)) ctas *= 2;
+    const long long half = (wanted / ctas + 1) / 2, warps = (half + 31) / 32;
+    const int threads = warps >= 32 ? 1024 : (int)warps * 32;
+    const long long rounds = (wanted + (long long)ctas * threads - 1) / ((long long)ctas * threads);
+    const int steps = rounds < kPlanSteps ? (int)rounds : kPlanSteps;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -893,10 +891,10 @@ cudaError_t decode_beams_launch(const BeamsArgs& args, const CUtensorMap& tq, co
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    e = a.K <= 4    ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<4>, a)
-        : a.K <= 8  ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<8>, a)
-        : a.K <= 16 ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<16>, a)
-                    : cudaLaunchKernelEx(&cfg, beams_plan_kernel<32>, a);
+    e = lanes == 4    ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<4>, a, steps)
+        : lanes == 8  ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<8>, a, steps)
+        : lanes == 16 ? cudaLaunchKernelEx(&cfg, beams_plan_kernel<16>, a, steps)
+                      : cudaLaunchKernelEx(&cfg, beams_plan_kernel<32>, a, steps);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)a.tc_grid);
     cfg.blockDim = dim3(kThreads);
