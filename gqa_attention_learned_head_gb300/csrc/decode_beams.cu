@@ -249,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int B = a.N, Hkv = a.Hkv, R = a.R, K = a.K, G = a.G;
     constexpr int kKeys = kBN / SPLIT;  // keys of a tile that a softmax thread takes
     constexpr int kBlock = kBM / SPLIT;  // rows of a copy of the query rows
+    constexpr int kBlocks = SPLIT == 1 ? kKeys / 32 : 1;  // parts of a thread's keys that are left out where no row sees them
     const int active = SPLIT > 1 ? 4 : (R + 31) / 32;  // softmax warps that hold rows
 
     // ---- 0. set-up that reads no input (barriers, tensor memory, the Q padding): done before the wait
@@ -458,6 +459,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                     issued = J + 1;
                 }
             }
+            if (is_k && lane == 0 && a.merge_list) {
+                // list the segment whose first piece this share holds without completing it (its last piece, if any): the
+                // split merge combines its partials once every CTA has finished
+                int2 head = make_int2(-1, 0);
+                if (ok && pc.ta == 0 && pc.tb < pc.tiles) {
+                    long long c_first = 0;
+                    int pieces = 0;
+                    segment_pieces(pc.seg_start, pc.tiles, C, U, c_first, pieces);
+                    head = make_int2(pc.b * Hkv + pc.g, pieces);
+                }
+                a.merge_list[cta] = head;
+            }
             if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
             // every copy this warp started has landed before the CTA can exit (bounded)
             if (lane == 0) {
@@ -547,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int copy = (tid - 128) / kBlock, r = (tid - 128) % kBlock;  // copy of the query rows, row
         const bool live = r < R;
         const int i = live ? r / G : 0, h = live ? r % G : 0;
-        int2 head = make_int2(-1, 0);  // the share's last piece, if it starts a segment it does not end
         if (warp - 4 < active) {
             // ---------------------------------------------------------------- softmax
             const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
@@ -560,56 +572,90 @@ __global__ void __launch_bounds__(kThreads, 2)
                 tmem_st32(tP + 32, zero);
                 tc_wait_st();
             }
+            auto store_p = [&](uint32_t (&pk)[kKeys / 2]) {
+                if constexpr (SPLIT == 4) {
+                    tmem_st16(tP + copy * 16, pk);
+                } else {
+#pragma unroll
+                    for (int cc = 0; cc < kKeys / 64; ++cc)
+                        tmem_st32(tP + copy * (kKeys / 2) + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[cc * 32]));
+                }
+            };
+            const uint32_t mine = live ? 1u << i : 0u;
+            bool blank = SPLIT > 1;    // this warp's weights are zeros
             int J = 0, p = 0, ex = 0;  // tiles, pieces, phases of the exchange barrier
             bool ok = true;
             const int sw = warp - 4;
-            while (ok) {
-                const Piece* next = next_piece(a, sm, sw, lane);
-                if (!next) break;
+            // the entries of a tile's pages are copied to shared memory one tile ahead (in registers they would not fit
+            // beside the scores, and a spill waits for the load)
+            const PageEntry* entries = nullptr;  // of the piece's group
+            auto fetch = [&](int t, int pages) {
+                const int e = t * kPagesPerTile + lane;
+                if (lane < kPagesPerTile) copy16_async(&sm.entry[sw][t & 1][lane], entries + (e < pages ? e : pages - 1));
+            };
+            // a piece's first entries, and this row's cached tokens (the plan kernel reported lengths out of range)
+            auto begin = [&](const Piece& pc) {
+                entries = a.entries + (long long)pc.b * K * a.max_pages;
+                fetch(pc.ta, pc.pages);
+                return live ? __ldcg(&a.kv_lens[(long long)pc.b * K + i]) : 0;
+            };
+            const Piece* next = next_piece(a, sm, sw, lane);
+            int cached = next ? begin(*next) : 0;
+            while (next) {
                 const Piece& pc = *next;
-                const int ta = pc.ta, tb = pc.tb, pages = pc.pages;
-                const PageEntry* entries = a.entries + (long long)pc.b * K * a.max_pages;
-                // the entries of a tile's pages are copied to shared memory one tile ahead (in registers they would not fit
-                // beside the scores, and a spill waits for the load)
-                auto fetch = [&](int t) {
-                    if (lane < kPagesPerTile) {
-                        const int e = t * kPagesPerTile + lane;
-                        copy16_async(&sm.entry[sw][t & 1][lane], entries + (e < pages ? e : pages - 1));
-                    }
-                };
-                fetch(ta);
-                // this row's cached tokens (the plan kernel reported lengths out of range)
-                const int len = live ? clamp_len(__ldcg(&a.kv_lens[(long long)pc.b * K + i]), a.max_pages * kPageSize) : 0;
-                const bool seeded = ta == 0 && copy == 0;
+                const int ta = pc.ta, tb = pc.tb, pages = pc.pages, seg = pc.b * Hkv + pc.g;
+                const bool starts = ta == 0, whole = starts && tb == pc.tiles;
+                const int len = clamp_len(cached, a.max_pages * kPageSize);
+                const bool seeded = starts && copy == 0;
                 float m = (seeded && live) ? __ldg(&a.sinks[pc.g * G + h]) * kLog2e : kNegInf;
                 float d = (seeded && live) ? 1.f : 0.f;  // the sink's own e^(sink - m) = 1
                 for (int t = ta; t < tb; ++t, ++J) {
                     copies_done();
                     __syncwarp();
                     const int4* entry = sm.entry[sw][t & 1];
-                    fetch(t + 1);
+                    if (t + 1 < tb) fetch(t + 1, pages);
                     // does any row of this warp's keys' pages see less than all of them?
                     constexpr int kMine = kKeys / kPageSize;  // pages of this copy's keys
                     const int page0 = copy * kMine, left = pages - t * kPagesPerTile - page0;
                     const bool masked =
                         left < kMine || !__all_sync(0xffffffffu, (entry[page0 + lane % kMine].w & kAllSee) != 0);
-                    // this row's visible keys: of each page, the slots its length reaches
-                    uint32_t vis[kKeys / 32];
+                    // this row's visible keys: of each page, the slots its length reaches; `use`: the blocks of 32 keys of
+                    // which some row of this warp sees any
+                    uint32_t vis[kKeys / 32], use = ~0u;
                     if (masked) {
+                        use = 0u;
 #pragma unroll
                         for (int w = 0; w < kKeys / 32; ++w) {
                             vis[w] = 0u;
 #pragma unroll
                             for (int half = 0; half < 2; ++half) {
                                 const int4 e = entry[page0 + 2 * w + half];
-                                const int n = len - kPageSize * e.y;
-                                const uint32_t bits = n >= kPageSize ? 0xFFFFu : (n > 0 ? (1u << n) - 1u : 0u);
-                                if (live && 2 * w + half < left && (((uint32_t)e.z >> i) & 1u)) vis[w] |= bits << (16 * half);
+                                const int n = max(0, min(kPageSize, len - kPageSize * e.y));
+                                const uint32_t bits = ((1u << n) - 1u) << (16 * half);
+                                if (((uint32_t)e.z & mine) && 2 * w + half < left) vis[w] |= bits;
                             }
+                            use |= __any_sync(0xffffffffu, vis[w] != 0u) ? 1u << w : 0u;
                         }
                     }
                     if (!(ok = warp_wait(&sm.s_full, J & 1))) break;
                     tc_fence_after();
+                    const bool first = t == ta;  // O starts afresh with this piece
+                    if (use == 0u) {  // pages of other warps' rows only: no weight changes
+                        mbar_arrive(&sm.s_free);
+                        if (!first) {
+                            if (!(ok = warp_wait(&sm.o_done, (J - 1) & 1))) break;
+                            tc_fence_after();
+                        }
+                        if (!blank) {
+                            uint32_t zero[kKeys / 2] = {};
+                            store_p(zero);
+                            tc_wait_st();
+                            blank = true;
+                        }
+                        tc_fence_before();
+                        mbar_arrive(&sm.p_full);
+                        continue;
+                    }
                     float s[kKeys];
 #pragma unroll
                     for (int cc = 0; cc < kKeys / 32; ++cc)
@@ -624,24 +670,36 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int cc = 0; cc < kKeys; ++cc) s[cc] *= scale_log2;
                         mul = 1.f;
                     }
-                    if (masked) {
+                    if (masked && kBlocks == 1) {
 #pragma unroll
                         for (int cc = 0; cc < kKeys; ++cc) s[cc] = ((vis[cc >> 5] >> (cc & 31)) & 1u) ? s[cc] : kNegInf;
                     }
-                    float acc[8];
+                    constexpr int kPer = kKeys / kBlocks;
+                    float mx_raw = kNegInf;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmax3(s[e], s[8 + e], s[16 + e]);
+                    for (int w = 0; w < kBlocks; ++w) {
+                        float* x = s + w * kPer;
+                        if (kBlocks > 1) {
+                            if (!((use >> w) & 1u)) continue;
+                            if (masked) {
 #pragma unroll
-                    for (int cc = 24; cc < kKeys - 8; cc += 16)
+                                for (int cc = 0; cc < kPer; ++cc) x[cc] = ((vis[w] >> cc) & 1u) ? x[cc] : kNegInf;
+                            }
+                        }
+                        float acc[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) acc[e] = fmax3(acc[e], s[cc + e], s[cc + 8 + e]);
+                        for (int e = 0; e < 8; ++e) acc[e] = fmax3(x[e], x[8 + e], x[16 + e]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], s[kKeys - 8 + e]);
-                    const float mx_raw =
-                        fmaxf(fmax3(acc[0], acc[1], acc[2]), fmax3(acc[3], acc[4], fmax3(acc[5], acc[6], acc[7])));
+                        for (int cc = 24; cc < kPer - 8; cc += 16)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) acc[e] = fmax3(acc[e], x[cc + e], x[cc + 8 + e]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) acc[e] = fmaxf(acc[e], x[kPer - 8 + e]);
+                        mx_raw = fmaxf(mx_raw, fmaxf(fmax3(acc[0], acc[1], acc[2]),
+                                                     fmax3(acc[3], acc[4], fmax3(acc[5], acc[6], acc[7]))));
+                    }
                     const float mx = mx_raw == kNegInf ? kNegInf : mx_raw * mul;
                     const float m_new = fmaxf(m, mx);
-                    const bool first = t == ta;  // O starts afresh with this piece
                     float factor = 1.f;
                     bool rescale_o = false;
                     if (first || m_new > m + kRescaleThreshold) {
@@ -656,11 +714,19 @@ __global__ void __launch_bounds__(kThreads, 2)
                                       make_float2(0.f, 0.f)};
                     uint32_t pk[kKeys / 2];
 #pragma unroll
-                    for (int cc = 0; cc < kKeys / 2; ++cc) {
-                        const float2 xx = ffma2(make_float2(s[2 * cc], s[2 * cc + 1]), mul2, negm2);
-                        const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
-                        sums[cc & 3] = fadd2(sums[cc & 3], pp);
-                        pk[cc] = pack_bf16(pp.x, pp.y);
+                    for (int w = 0; w < kKeys / 32; ++w) {
+                        if (kBlocks == 1 || ((use >> w) & 1u)) {
+#pragma unroll
+                            for (int cc = 16 * w; cc < 16 * w + 16; ++cc) {
+                                const float2 xx = ffma2(make_float2(s[2 * cc], s[2 * cc + 1]), mul2, negm2);
+                                const float2 pp = make_float2(fast_exp2(xx.x), fast_exp2(xx.y));
+                                sums[cc & 3] = fadd2(sums[cc & 3], pp);
+                                pk[cc] = pack_bf16(pp.x, pp.y);
+                            }
+                        } else {
+#pragma unroll
+                            for (int cc = 16 * w; cc < 16 * w + 16; ++cc) pk[cc] = 0u;
+                        }
                     }
                     const float2 s01 = fadd2(fadd2(sums[0], sums[1]), fadd2(sums[2], sums[3]));
                     d += s01.x + s01.y;
@@ -679,20 +745,17 @@ __global__ void __launch_bounds__(kThreads, 2)
                             }
                         }
                     }
-                    if constexpr (SPLIT == 4) {
-                        tmem_st16(tP + copy * 16, pk);
-                    } else {
-#pragma unroll
-                        for (int cc = 0; cc < kKeys / 64; ++cc)
-                            tmem_st32(tP + copy * (kKeys / 2) + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[cc * 32]));
-                    }
+                    store_p(pk);
+                    blank = false;
                     tc_wait_st();
                     tc_fence_before();
                     mbar_arrive(&sm.p_full);
                 }
-                copies_done();  // the entries fetched last land before their slot is fetched into again
-                __syncwarp();
                 if (!ok) break;
+                const long long row0 = (long long)pc.b * K * a.Hq + pc.g * G;
+                // the next piece is looked up while the last product runs
+                next = next_piece(a, sm, sw, lane);
+                if (next) cached = begin(*next);
                 // ---- end of the piece (the PV of its last tile has finished): O / d of this row
                 if (!(ok = warp_wait(&sm.o_done, (J - 1) & 1))) break;
                 tc_fence_after();
@@ -710,8 +773,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if constexpr (SPLIT > 1) {
                     // the copies' sums of a row, brought to one maximum, are added up: each thread gives the dims that it
                     // does not finish to the thread of the same row in another copy
+                    // (through the piece's Q slot, which is free: its scores are done)
                     const int t0 = tid - 128;
+                    float(*give)[kBM] = reinterpret_cast<float(*)[kBM]>(sm.q[p & 1]);
+                    const bool upper = copy & 1;
                     sm.md[t0] = make_float2(m, d);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) give[e][t0] = upper ? o[e] : o[32 + e];
                     mbar_arrive(&sm.exchange);
                     if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
                     float M = m, D = 0.f;
@@ -722,21 +790,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const float2 x = sm.md[c * kBlock + r];
                         D += x.x == kNegInf ? 0.f : x.y * fast_exp2(x.x - M);
                     }
-                    scale_o = (m == kNegInf || !(D > 0.f)) ? 0.f : fast_exp2(m - M) / D;
                     // (all mass on nothing: a sink of -inf and no key)
                     l2 = D > 0.f ? M + log2f(D) : kNegInf;
+                    auto share = [&](float mc) { return (mc == kNegInf || !(D > 0.f)) ? 0.f : fast_exp2(mc - M) / D; };
+                    const float ours = share(m), theirs = share(sm.md[t0 ^ kBlock].x);
 #pragma unroll
-                    for (int e = 0; e < 64; ++e) o[e] *= scale_o;
+                    for (int e = 0; e < 32; ++e) o[e] = (upper ? o[32 + e] : o[e]) * ours + give[e][t0 ^ kBlock] * theirs;
                     scale_o = 1.f;
-                    // the piece's Q slot is free (its scores are done) and takes the first exchange
-                    float(*give)[kBM] = reinterpret_cast<float(*)[kBM]>(sm.q[p & 1]);
-                    const bool upper = copy & 1;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) give[e][t0] = upper ? o[e] : o[32 + e];
-                    mbar_arrive(&sm.exchange);
-                    if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = (upper ? o[32 + e] : o[e]) + give[e][t0 ^ kBlock];
                     dim0 = upper ? 32 : 0;
                     fence_proxy_async_smem();  // before a copy of query rows may land there
                     mbar_arrive(&sm.q_empty[p & 1]);
@@ -752,17 +812,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     ++p;
                 }
-                const bool starts = ta == 0, whole = starts && tb == pc.tiles;
-                const int seg = pc.b * Hkv + pc.g;
-                if (starts && !whole) {
-                    long long c_first = 0;
-                    int pieces = 0;
-                    segment_pieces(pc.seg_start, pc.tiles, C, U, c_first, pieces);
-                    head = make_int2(seg, pieces);
-                }
                 if (live) {
                     if (whole) {
-                        const long long row = ((long long)pc.b * K + i) * a.Hq + pc.g * G + h;
+                        const long long row = row0 + (long long)i * a.Hq + h;
                         uint4* dst = reinterpret_cast<uint4*>(a.out + row * kHeadDim + dim0);
 #pragma unroll
                         for (int e = 0; e < kDims / 8; ++e) {
@@ -785,11 +837,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             }
+            copies_done();
             if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
         }
-        // ---- list the segment whose first piece this share holds without completing it (the
-        // split merge combines its partials once every CTA has finished)
-        if (tid == 128 && a.merge_list) a.merge_list[cta] = head;
     }
     tc_fence_before();
     __syncthreads();
