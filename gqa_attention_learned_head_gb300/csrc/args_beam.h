@@ -29,7 +29,7 @@ struct BeamArgs {
     unsigned* err;
     long long row_stride;
     int N, K, V, M, pad_token, dtype;
-    int parts, part_len;        // CTAs per row, tokens of each (a multiple of 16; the last may have fewer)
+    int parts, part_len;        // CTAs per row, tokens of each (a multiple of 32; the last may have fewer)
 };
 struct BeamPlan {
     int parts, part_len;

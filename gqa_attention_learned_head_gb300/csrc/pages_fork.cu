@@ -17,7 +17,12 @@
 // rows every CTA goes over all of them by itself, in shared memory, and the cluster meets once.
 // fork_apply_kernel: a thread takes a column or some of kBatch present and kBatch new rows, reads and writes their
 // entries, and adds up the changes to the count of a page that several of them hold: for the pages that a group's
-// rows share, drops and forks mostly cancel and no atomic is left.  Bound by the table's bytes.
+// rows share, drops and forks mostly cancel and no atomic is left.  Its loads are latency too: a group's rows are read
+// together, and a quarter of the time is the table's bytes.
+//
+// Measured (GB300): 256 groups of 8 rows of 1024 to 32768 tokens (27.8 MB: 4.1 us at the copy rate) 24.0 us, 12.5 in the
+// plan and 11.5 in the application; 4 rows of one group 7.3 us.  The simplest form
+// (an atomic for every holder that comes or goes) took 54 us.
 #include "args_pages.h"
 #include "ptx.cuh"
 

@@ -429,8 +429,9 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
 /*
  * Beam search's selection: of the K x V continuations of each group, the M of the highest score
  *     score(k, v) = scores[n][k] + logits[n][k][v] - ln sum_u exp(logits[n][k][u]),
- * in descending order; equal scores go to the lower beam, then the lower token.  Scores are compared in
- * 64 bits (sums of exponentials in 32 bits per thread and 64 across threads).
+ * in descending order; equal scores go to the lower beam, then the lower token.  Sums of exponentials are
+ * held in 32 bits per thread (of at most 1024 tokens); everything above that, and the scores that are
+ * compared, in pairs of floats (48 bits); out_scores are those rounded to f32.
  *
  *   logits    [N, K, V]  f32, bf16 or f16; row (n, k) starts row_stride elements after row (n, k - 1)
  *   scores    [N, K]     f32   running log-probability of each beam; -inf: the beam is not in use, its
@@ -446,6 +447,8 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
  * A logit of -inf is no continuation.  Where a group has fewer than M, the rest of its row is score -inf,
  * parent -1, token -1.  A beam in use whose score is NaN or +inf, or whose logits hold a NaN or +inf, has
  * no continuation and raises SINKATTN_ERR_BAD_VALUE.
+ * K * M * ceil(V / 262144) above 4096 (candidates of a group that meet in one block) is
+ * SINKATTN_ERR_UNSUPPORTED.
  */
 sinkattn_status_t sinkattn_beam_select(const void *logits, const float *scores, const uint8_t *finished,
                                        float *out_scores, int32_t *out_parents, int32_t *out_tokens,

@@ -1,10 +1,12 @@
 """Beam search's selection on the GPU against numpy in 64 bits, through the C ABI.
 
-Tolerance.  A thread adds at most 65536 / 16 / 256 groups of 16 exponentials into four 32-bit sums, 64 additions
-each: 64 x 2^-24 relative in the worst case; an exponential is off by 2^-22 (the instruction's bound) plus 2^-24 times
-its argument, whose terms weigh e^argument (x e^-x <= 0.37); the groups' order adds nothing.  Together the log-sum-exp is
-off by at most 5e-6, and a returned 32-bit score by that plus half a step of its own.  Picks have to be the reference's
-wherever its next score is further away than twice that.
+Tolerance.  The largest share of a row here is 131104 tokens: each of 256 threads adds up to 528 exponentials into
+four 32-bit sums, 132 additions each.  An addition is off by at most 2^-24 of the partial sum, which grows from 0 to the
+whole, so for terms in no order 67 x 2^-24 = 4.0e-6 relative, were all 1024 sums to lean one way (shares of up to 65536
+tokens, all other tests: 64 additions and 3.8e-6 even if each is off by 2^-24 of the whole).  An exponential is off by
+2^-22 (the instruction's bound) plus 2^-24 times its argument, whose terms weigh e^argument (x e^-x <= 0.37); the groups'
+order adds nothing.  Together the log-sum-exp is off by at most 5e-6, and a returned 32-bit score by that plus half a step
+of its own.  Picks have to be the reference's wherever its next score is further away than twice that.
 """
 import math
 
