@@ -299,6 +299,8 @@ sinkattn_status_t sinkattn_decode_beams(const void* q, const void* k_pages, cons
         return SINKATTN_ERR_INVALID_ARG;
     BeamsArgs a;
     a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k_pages = static_cast<const __nv_bfloat16*>(k_pages);
+    a.v_pages = static_cast<const __nv_bfloat16*>(v_pages);
     a.page_table = page_table;
     a.kv_lens = kv_lens;
     a.sinks = sinks;

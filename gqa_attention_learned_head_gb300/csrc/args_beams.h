@@ -20,6 +20,8 @@ constexpr int kAllSee = 32;
 
 struct BeamsArgs {
     const __nv_bfloat16* q;     // [N, K, Hq, 64]
+    const __nv_bfloat16* k_pages;  // [P, Hkv, 16, 64]
+    const __nv_bfloat16* v_pages;
     const int32_t* page_table;  // [N, K, max_pages]
     const int32_t* kv_lens;     // [N, K]
     const float* sinks;         // [Hq]

@@ -27,6 +27,8 @@
 // softmax warps work then: with 8 rows of 8 heads over one long prompt the call took 186 us instead of 202.
 // A row's own pages are weights of zero for every other row of the group: a warp whose rows see none of its keys of a
 // tile takes no maximum and no exponential of them.
+// A weight of zero times a NaN or an infinity in such a page is a NaN in rows that do not hold it: rows whose sums come
+// out not finite are taken again one by one at the share's end (out of line: in line its registers cost the whole 3 us).
 // The piece with a segment's first tile is seeded with the sink.  The pieces of a segment split between CTAs
 // write fp32 partials; the CTA holding the segment's first piece lists it, and the split-merge kernel, launched
 // right behind this one as a programmatic dependent, combines them (merging in the CTA that finishes a segment's last
@@ -216,7 +218,7 @@ struct __align__(1024) Smem {
     uint32_t tmem_base;
     long long red[8];    // block reductions
     long long found[4];  // share start: group, its first unit, its pages, flag
-    Walk walk[4];        // the softmax warps' walkers (kept out of their registers)
+    Walk walk[5];        // the softmax warps' walkers (kept out of their registers), and the share's start
     Piece piece[4];      // ... and their current pieces
     int4 entry[4][2][kPagesPerTile];  // the softmax warps' page entries, this tile's and the next one's
     float2 md[kBM];                   // SPLIT > 1: running maximum and normaliser of every thread at a piece's end
@@ -247,6 +249,95 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
         : "memory");
 }
 
+// One row's attention over its own pages among those of the piece, by a whole warp from global memory: the output's dims
+// 2 lane and 2 lane + 1.  Two lanes take a slot's key, half of its dims each.
+__device__ __forceinline__ float2 row_alone(const BeamsArgs& a, const Piece& pc, int row, int lane) {
+    const int i = row / a.G, head = pc.g * a.G + row % a.G, slot = lane & 15;
+    const long long beam = (long long)pc.b * a.K + i;
+    const int len = clamp_len(__ldcg(&a.kv_lens[beam]), a.max_pages * kPageSize);
+    const uint4* q = reinterpret_cast<const uint4*>(a.q + (beam * a.Hq + head) * kHeadDim) + 4 * (lane >> 4);
+    float m = pc.ta == 0 ? __ldg(&a.sinks[head]) * kLog2e : kNegInf, d = pc.ta == 0 ? 1.f : 0.f;
+    float2 sum = make_float2(0.f, 0.f);
+    const int end = min(pc.pages, pc.tb * kPagesPerTile);
+    for (int e = pc.ta * kPagesPerTile; e < end; ++e) {
+        const PageEntry x = entry_of(a, pc.b, e);
+        const int n = min(kPageSize, len - kPageSize * x.col);  // its keys in this page
+        if (!((x.beams >> i) & 1u) || n <= 0) continue;
+        const long long at = ((long long)x.page * a.Hkv + pc.g) * (kPageSize * kHeadDim);
+        float dot = 0.f;
+        if (slot < n) {
+            const uint4* k = reinterpret_cast<const uint4*>(a.k_pages + at + slot * kHeadDim) + 4 * (lane >> 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 u = __ldcg(k + j), w = __ldcg(q + j);
+                const uint32_t ku[4] = {u.x, u.y, u.z, u.w}, qw[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    dot = fmaf(__uint_as_float(ku[c] << 16), __uint_as_float(qw[c] << 16), dot);
+                    dot = fmaf(__uint_as_float(ku[c] & 0xffff0000u), __uint_as_float(qw[c] & 0xffff0000u), dot);
+                }
+            }
+        }
+        dot += __shfl_xor_sync(0xffffffffu, dot, 16);
+        const float s = slot < n ? dot * a.scale_log2 : kNegInf;
+        float top = fmaxf(m, s);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float keep = m == kNegInf ? 0.f : fast_exp2(m - top), w = slot < n ? fast_exp2(s - top) : 0.f;
+        m = top;
+        float all = w;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        d = d * keep + all;
+        sum.x *= keep;
+        sum.y *= keep;
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(a.v_pages + at) + lane;
+#pragma unroll
+        for (int j = 0; j < kPageSize; ++j) {
+            const uint32_t u = j < n ? __ldcg(v + j * (kHeadDim / 2)) : 0u;
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            sum.x = fmaf(wj, __uint_as_float(u << 16), sum.x);
+            sum.y = fmaf(wj, __uint_as_float(u & 0xffff0000u), sum.y);
+        }
+    }
+    return d == 0.f ? make_float2(0.f, 0.f) : make_float2(sum.x / d, sum.y / d);
+}
+
+// The rows of a softmax warp whose sums in some piece of the share are not finite, taken again by themselves over the pages
+// that they hold; `again` is the walk at the share's start.
+template <int SPLIT>
+__device__ __noinline__ void rows_alone(const BeamsArgs& a, Walk again) {
+    constexpr int kBlock = kBM / SPLIT, kDims = kHeadDim / SPLIT;
+    const int t0 = (int)threadIdx.x - 128, lane = t0 & 31, copy = t0 / kBlock, r = t0 % kBlock, R = a.R, G = a.G;
+    const int dim0 = (SPLIT > 1 && (copy & 1) ? 32 : 0) + (SPLIT > 2 && (copy & 2) ? 16 : 0);
+    Piece pc;
+    while (again.next(a, pc)) {
+        const bool whole = pc.ta == 0 && pc.tb == pc.tiles;
+        const long long row0 = whole ? (long long)pc.b * a.K * a.Hq + pc.g * G
+                                     : ((long long)blockIdx.x + pc.b * a.Hkv + pc.g) * R;
+        auto place = [&](int row) {  // its first value in out or in the partials
+            return (row0 + (whole ? (long long)(row / G) * a.Hq + row % G : row)) * kHeadDim;
+        };
+        bool redo = false;
+        if (r < R) {
+            const long long at = place(r) + dim0;
+            for (int e = 0; e < kDims; ++e) {
+                const float x = whole ? __bfloat162float(a.out[at + e]) : a.part_o[at + e];
+                redo |= !(x * 0.f == 0.f);
+            }
+        }
+        __syncwarp();
+        for (unsigned left = __ballot_sync(0xffffffffu, redo); left; left &= left - 1) {
+            const int from = __ffs(left) - 1, row = __shfl_sync(0xffffffffu, r, from);
+            const int lo = __shfl_sync(0xffffffffu, dim0, from);
+            const float2 x = row_alone(a, pc, row, lane);
+            if (2 * lane < lo || 2 * lane >= lo + kDims) continue;
+            const long long at = place(row) + 2 * lane;
+            if (whole) *reinterpret_cast<uint32_t*>(a.out + at) = pack_bf16(x.x, x.y);
+            else *reinterpret_cast<float2*>(a.part_o + at) = x;
+        }
+    }
+}
 
 template <int SPLIT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -409,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     walk.seg_start = sm.found[1] + (long long)walk.g * walk.tiles;
     walk.x = x0;
     walk.x1 = x1;
-    if (tid < 4) sm.walk[tid] = walk;
+    if (tid < 5) sm.walk[tid] = walk;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -592,6 +683,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             const uint32_t mine = live ? 1u << i : 0u;
             bool blank = SPLIT > 1;    // this warp's weights are zeros
+            // the dims of its row that a thread finishes (see the exchange below)
+            constexpr int kDims = kHeadDim / SPLIT;
+            const int dim0 = (SPLIT > 1 && (copy & 1) ? 32 : 0) + (SPLIT > 2 && (copy & 2) ? 16 : 0);
+            bool odd = false;          // a sum that is not finite
             int J = 0, p = 0, ex = 0;  // tiles, pieces, phases of the exchange barrier
             bool ok = true;
             const int sw = warp - 4;
@@ -777,8 +872,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int e = 0; e < 64; ++e) o[e] = __uint_as_float(raw[e]);
                 float scale_o = d > 0.f ? 1.f / d : 0.f, l2 = d > 0.f ? m + log2f(d) : kNegInf;
-                constexpr int kDims = kHeadDim / SPLIT;  // dims of the row that this thread finishes
-                int dim0 = 0;
                 if constexpr (SPLIT > 1) {
                     // the copies' sums of a row, brought to one maximum, are added up: each thread gives the dims that it
                     // does not finish to the thread of the same row in another copy
@@ -806,7 +899,6 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = (upper ? o[32 + e] : o[e]) * ours + give[e][t0 ^ kBlock] * theirs;
                     scale_o = 1.f;
-                    dim0 = upper ? 32 : 0;
                     fence_proxy_async_smem();  // before a copy of query rows may land there
                     mbar_arrive(&sm.q_empty[p & 1]);
                     if constexpr (SPLIT == 4) {
@@ -817,10 +909,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (!(ok = warp_wait(&sm.exchange, ex++ & 1))) break;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = (upper2 ? o[16 + e] : o[e]) + sm.half[e][t0 ^ (2 * kBlock)];
-                        dim0 += upper2 ? 16 : 0;
                     }
                     ++p;
                 }
+                float probe = 0.f;  // a NaN if any of the sums is not finite
+#pragma unroll
+                for (int e = 0; e < kDims; ++e) probe = fmaf(o[e], 0.f, probe);
+                odd |= live && probe * scale_o != 0.f;
                 if (live) {
                     if (whole) {
                         const long long row = row0 + (long long)i * a.Hq + h;
@@ -847,6 +942,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             copies_done();
+            // a weight of zero times a NaN or infinity in another row's page is a NaN (nothing waits for this warp any
+            // more but the CTA's end)
+            if (ok && __any_sync(0xffffffffu, odd)) rows_alone<SPLIT>(a, sm.walk[4]);
             if (!ok && lane == 0) atomicOr(a.err, kErrTimeout);
         }
     }

@@ -120,6 +120,39 @@ def test_scales(S, scale):
     check(S, *make(16, 2, [[40, 17, 129]], seed=33), what=f"scale={scale}", scale=scale)
 
 
+@pytest.mark.parametrize("Hq,Hkv,K", [(8, 1, 3), (64, 8, 8), (64, 8, 16), (5, 1, 6)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("workers", [0, 7])
+def test_poisoned_row(S, Hq, Hkv, K, value, workers):
+    """A value that is not finite in a row's own pages stays that row's, whichever rows its tiles hold besides."""
+    lens = [[300 - 7 * k for k in range(K)], [40] * K, [1200] * K]
+    q, k, v, table, lens, sinks = make(Hq, Hkv, lens, seed=K, share="tree")
+    ro, rl = ref(q, k, v, table, lens, sinks)
+    hit = torch.zeros(3, K, dtype=torch.bool)
+    for n in range(3):
+        last = (int(lens[n, 1]) - 1) // PS  # row 1's last page: every column this late is a row's own
+        page = int(table[n, 1, last])
+        hit[n] = (table[n, :, last] == page)
+        v[page, :, 0, 5] = value
+        v[page, :, 1, 50] = value
+    assert hit.any(1).all() and not hit.all(1).any()
+    out, lse, err = run(S, q, k, v, table, lens, sinks, num_workers=workers)
+    assert err == 0
+    out, lse = out.float().cpu(), lse.cpu()
+    assert not torch.isfinite(out[hit][..., 5]).any() and not torch.isfinite(out[hit][..., 50]).any()
+    assert_parity(out[~hit].numpy(), lse[~hit].numpy(), torch.as_tensor(ro)[~hit].numpy(), torch.as_tensor(rl)[~hit].numpy(),
+                  f"{Hq} {Hkv} {K} {value}")
+    # ... and a key that is not finite: its row's scores only
+    v[~torch.isfinite(v.float())] = 0
+    for n in range(3):
+        k[int(table[n, 1, (int(lens[n, 1]) - 1) // PS]), :, 0] = value
+    ro, rl = ref(q, k, v, table, lens, sinks)
+    out, lse, err = run(S, q, k, v, table, lens, sinks, num_workers=workers)
+    assert err == 0
+    assert_parity(out.float().cpu()[~hit].numpy(), lse.cpu()[~hit].numpy(), torch.as_tensor(ro)[~hit].numpy(),
+                  torch.as_tensor(rl)[~hit].numpy(), f"key {Hq} {Hkv} {K} {value}")
+
+
 def test_rising_scores(S):
     """Scores that grow along the cache: the running maximum is exceeded again and again, in whole and split groups."""
     q, k, v, table, lens, sinks = make(16, 2, [[2000, 1990, 2000, 1500]], seed=34, share="tree")
