@@ -438,7 +438,7 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
  *                              logits are not read and it has no continuation
  *   finished  [N, K]     uint8 or NULL: a beam with a non-zero flag has one continuation, pad_token at its
  *                              unchanged score; its logits are not read
- *   out_scores  [N, M]   f32
+ *   out_scores  [N, M]   f32   may be scores itself where M = K
  *   out_parents [N, M]   int32 row n * K + k of the beam continued (as sinkattn_pages_fork takes it)
  *   out_tokens  [N, M]   int32
  *   workspace  at least sinkattn_beam_select_workspace_size(dims) bytes, 256-byte aligned; it needs no

@@ -288,3 +288,14 @@ def test_refusals(S):
     with pytest.raises(S.SinkAttnError) as e:
         S.sinkattn_beam_select(z, c, 4, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert e.value.status == S.ERR_WORKSPACE
+
+
+def test_scores_in_place(S):
+    """The running scores of the next step over those of this one."""
+    z, c = make(70, 6, 9001, torch.bfloat16, seed=23)
+    want = S.sinkattn_beam_select(z, c, 6)
+    kept = c.clone()
+    got = S.sinkattn_beam_select(z, kept, 6, out_scores=kept)
+    assert got[0].data_ptr() == kept.data_ptr()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert S.sinkattn_get_error() == 0
