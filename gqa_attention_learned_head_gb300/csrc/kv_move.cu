@@ -8,7 +8,7 @@
 //
 // Measured (GB300): 4096 whole pages of 8 KV heads (268 MB moved) 41.8 us, 6.4 TB/s = 95% of the copy rate; 16
 // accepted tokens of 256 requests in 24 layers (214 MB) 32.5 us, 6.6 TB/s = 97%; 256 tails of a page 2.8 us, 32 trees
-// of 8 tokens 2.2 us, both little more than an empty kernel's.
+// of 8 tokens 2.2 us, both little more than the latency of one kernel.
 #include "args_pages.h"
 #include "ptx.cuh"
 
