@@ -347,9 +347,10 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
 
 
 # ---- a beam step over the paged cache -------------------------------------------------------------
-# These calls are short on the GPU, so their host path is kept short: plain integers instead of pointer objects, and
-# the raw handle of the current stream.
+# These calls are short on the GPU, so their host path is kept short: plain integers instead of pointer objects, the raw
+# handle of the current stream, and one test per tensor where nothing is wrong.
 
+_Tensor, _f32, _bf16, _i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
 _LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
 
 
@@ -365,13 +366,18 @@ def _on_stream(fn):
     return call
 
 
-def _here(*tensors):
-    """The index of the current device, on which all the tensors lie (the one the call's stream belongs to)."""
-    current = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != current:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{current}")
-    return current
+def _here(t, device):
+    """Refuses a tensor on another device than the current one, ``device``, to which the call's stream belongs."""
+    if t.get_device() != device:
+        raise ValueError(f"tensor on {t.device}, but the current device is cuda:{device}")
+
+
+def _arg(t, name, dtype, ndim, device):
+    """A contiguous tensor of this type and rank on ``device``, or an error."""
+    if (type(t) is _Tensor and t.get_device() == device and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()):
+        return
+    _need(t, name, dtype, ndim)
+    _here(t, device)
 
 
 def _at(t):
@@ -379,24 +385,23 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _out(t, name, dtype, shape, like):
+def _out(t, name, dtype, shape, like, device):
     """An output: the given tensor, checked, or a new one."""
     if t is None:
         return torch.empty(shape, device=like.device, dtype=dtype)
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != shape:
+    _arg(t, name, dtype, len(shape), device)
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    _here(t)
     return t
 
 
-def _room(workspace, nbytes, like):
+def _room(workspace, nbytes, like, device):
     """(workspace, its bytes): the caller's, or a new one of ``nbytes``."""
     if workspace is None:
         return torch.empty(nbytes, device=like.device, dtype=torch.uint8), nbytes
     if not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    _here(workspace)
+    _here(workspace, device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -419,37 +424,41 @@ def sinkattn_beam_select(logits, scores, num_select, finished=None, pad_token=0,
     [N, K] f32 running log-probabilities, finished [N, K] bool or uint8.  Returns (scores [N, M] f32, parents [N, M]
     int32 rows n * K + k, tokens [N, M] int32), best first.
     """
-    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+    device = torch._C._cuda_getDevice()
+    if not isinstance(logits, _Tensor) or not logits.is_cuda:
         raise TypeError("logits must be a CUDA tensor")
-    if logits.dtype not in _LOGIT_DTYPES:
+    dtype = _LOGIT_DTYPES.get(logits.dtype)
+    if dtype is None:
         raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
-    if logits.dim() != 3 or logits.shape[1] == 0 or logits.shape[2] == 0:
+    if logits.dim() != 3 or 0 in logits.shape[1:]:
         raise ValueError(f"logits must be [N, K, V], got shape {tuple(logits.shape)}")
-    N, K, V = logits.shape
-    if not logits.is_contiguous() and ((V > 1 and logits.stride(2) != 1) or
-                                       (N > 1 and K > 1 and logits.stride(0) != K * logits.stride(1))):
-        raise ValueError("logits must have contiguous tokens and rows at one distance from each other")
-    _need(scores, "scores", torch.float32, 2)
-    if scores.shape != (N, K):
+    N, K, V = shape = logits.shape
+    if logits.is_contiguous():
+        stride = V
+    else:
+        stride = logits.stride(1) if K > 1 else (logits.stride(0) if N > 1 else V)
+        if (V > 1 and logits.stride(2) != 1) or (N > 1 and K > 1 and logits.stride(0) != K * stride):
+            raise ValueError("logits must have contiguous tokens and rows at one distance from each other")
+    _here(logits, device)
+    _arg(scores, "scores", _f32, 2, device)
+    if scores.shape != shape[:2]:
         raise ValueError("scores must be [N, K]")
     if finished is not None:
-        _need(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, 2)
-        if finished.shape != (N, K):
+        _arg(finished, "finished", torch.bool if finished.dtype is torch.bool else torch.uint8, 2, device)
+        if finished.shape != shape[:2]:
             raise ValueError("finished must be [N, K]")
-    device = _here(logits, scores, finished)
     M = int(num_select)
-    dims = beam_dims(logits, M, int(pad_token))
-    ref = ctypes.byref(dims)
-    nbytes = _lib.sinkattn_beam_select_workspace_size(ref)
+    dims = BeamDims(N, K, V, M, dtype, int(pad_token), stride)
+    nbytes = _lib.sinkattn_beam_select_workspace_size(dims)
     if nbytes == 0:  # invalid dims: the call says why
-        st = _lib.sinkattn_beam_select(None, None, None, None, None, None, ref, None, 0, None)
+        st = _lib.sinkattn_beam_select(None, None, None, None, None, None, dims, None, 0, None)
         raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_beam_select")
-    out_scores = _out(out_scores, "out_scores", torch.float32, (N, M), logits)
-    out_parents = _out(out_parents, "out_parents", torch.int32, (N, M), logits)
-    out_tokens = _out(out_tokens, "out_tokens", torch.int32, (N, M), logits)
-    workspace, nbytes = _room(workspace, nbytes, logits)
+    out_scores = _out(out_scores, "out_scores", _f32, (N, M), scores, device)
+    out_parents = _out(out_parents, "out_parents", _i32, (N, M), scores, device)
+    out_tokens = _out(out_tokens, "out_tokens", _i32, (N, M), scores, device)
+    workspace, nbytes = _room(workspace, nbytes, scores, device)
     st = _lib.sinkattn_beam_select(logits.data_ptr(), scores.data_ptr(), _at(finished), out_scores.data_ptr(),
-                                   out_parents.data_ptr(), out_tokens.data_ptr(), ref, workspace.data_ptr(), nbytes,
+                                   out_parents.data_ptr(), out_tokens.data_ptr(), dims, workspace.data_ptr(), nbytes,
                                    _raw_stream(device))
     if st != OK:
         raise SinkAttnError(st, "sinkattn_beam_select")
@@ -466,61 +475,63 @@ def sinkattn_pages_fork(page_table, held_lens, parents, page_refs, keep_lens=Non
     max_pages], lens [R_out], refs [P], copies [R_out, 3]); ``copies`` goes to sinkattn_kv_copy before the new tokens
     are written.
     """
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(held_lens, "held_lens", torch.int32, 1)
-    _need(parents, "parents", torch.int32, 1)
-    _need(page_refs, "page_refs", torch.int32, 1)
+    device = torch._C._cuda_getDevice()
+    _arg(page_table, "page_table", _i32, 2, device)
+    _arg(held_lens, "held_lens", _i32, 1, device)
+    _arg(parents, "parents", _i32, 1, device)
+    _arg(page_refs, "page_refs", _i32, 1, device)
     Rin, mp = page_table.shape
-    R, P = parents.shape[0], page_refs.shape[0]
+    (R,), (P,) = parents.shape, page_refs.shape
     if held_lens.shape[0] != Rin:
         raise ValueError("held_lens must have one entry per row of page_table")
-    for t, name in ((keep_lens, "keep_lens"), (room_lens, "room_lens")):
-        if t is not None:
-            _need(t, name, torch.int32, 1)
-            if t.shape[0] != R:
-                raise ValueError(f"{name} must have one entry per new row")
-    device = _here(page_table, held_lens, parents, page_refs, keep_lens, room_lens)
+    if keep_lens is not None:
+        _arg(keep_lens, "keep_lens", _i32, 1, device)
+    if room_lens is not None:
+        _arg(room_lens, "room_lens", _i32, 1, device)
+    if (keep_lens is not None and keep_lens.shape[0] != R) or (room_lens is not None and room_lens.shape[0] != R):
+        raise ValueError("keep_lens and room_lens must have one entry per new row")
     dims = ForkDims(Rin, R, P, mp, 16, int(grow))
-    ref = ctypes.byref(dims)
-    nbytes = _lib.sinkattn_pages_fork_workspace_size(ref)
+    nbytes = _lib.sinkattn_pages_fork_workspace_size(dims)
     if nbytes == 0:  # invalid dims: the call says why
-        st = _lib.sinkattn_pages_fork(*[None] * 10, ref, None, 0, None)
+        st = _lib.sinkattn_pages_fork(*[None] * 10, dims, None, 0, None)
         raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_pages_fork")
-    out_table = _out(out_table, "out_table", torch.int32, (R, mp), page_table)
-    out_lens = _out(out_lens, "out_lens", torch.int32, (R,), page_table)
-    out_refs = _out(out_refs, "out_refs", torch.int32, (P,), page_table)
-    copies = _out(copies, "copies", torch.int32, (R, 3), page_table)
-    workspace, nbytes = _room(workspace, nbytes, page_table)
+    out_table = _out(out_table, "out_table", _i32, (R, mp), page_table, device)
+    out_lens = _out(out_lens, "out_lens", _i32, (R,), page_table, device)
+    out_refs = _out(out_refs, "out_refs", _i32, (P,), page_table, device)
+    copies = _out(copies, "copies", _i32, (R, 3), page_table, device)
+    workspace, nbytes = _room(workspace, nbytes, page_table, device)
     st = _lib.sinkattn_pages_fork(page_table.data_ptr(), held_lens.data_ptr(), parents.data_ptr(), _at(keep_lens),
                                   _at(room_lens), page_refs.data_ptr(), out_table.data_ptr(), out_lens.data_ptr(),
-                                  out_refs.data_ptr(), copies.data_ptr(), ref, workspace.data_ptr(), nbytes,
+                                  out_refs.data_ptr(), copies.data_ptr(), dims, workspace.data_ptr(), nbytes,
                                   _raw_stream(device))
     if st != OK:
         raise SinkAttnError(st, "sinkattn_pages_fork")
     return out_table, out_lens, out_refs, copies
 
 
-def _pools(k_pages, v_pages):
+def _pools(k_pages, v_pages, device):
     """The pools as [L, P, Hkv, 16, 64]; one layer's pool may come without its first dimension."""
-    _need(k_pages, "k_pages", torch.bfloat16, 5 if k_pages.dim() == 5 else 4)
-    _need(v_pages, "v_pages", torch.bfloat16, k_pages.dim())
-    if v_pages.shape != k_pages.shape:
+    ndim = 5 if k_pages.dim() == 5 else 4
+    _arg(k_pages, "k_pages", _bf16, ndim, device)
+    _arg(v_pages, "v_pages", _bf16, ndim, device)
+    shape = k_pages.shape
+    if v_pages.shape != shape:
         raise ValueError("k_pages and v_pages must have the same shape")
-    return k_pages.shape if k_pages.dim() == 5 else (1, *k_pages.shape)
+    return shape if ndim == 5 else (1, *shape)
 
 
 @_on_stream
 def sinkattn_kv_copy(k_pages, v_pages, copies):
     """Copies the first ``tokens`` slots of page src to page dst for every (src, dst, tokens) of copies [n, 3] int32,
     in place; k_pages / v_pages [P, Hkv, 16, 64] or, for several layers, [L, P, Hkv, 16, 64]."""
-    L, P, Hkv, PS, D = _pools(k_pages, v_pages)
-    _need(copies, "copies", torch.int32, 2)
-    if copies.shape[1] != 3:
+    device = torch._C._cuda_getDevice()
+    L, P, Hkv, PS, D = _pools(k_pages, v_pages, device)
+    _arg(copies, "copies", _i32, 2, device)
+    n, three = copies.shape
+    if three != 3:
         raise ValueError("copies must be [n, 3]")
-    device = _here(k_pages, v_pages, copies)
-    dims = MoveDims(L, copies.shape[0], Hkv, D, PS, P, 0, 0)
-    st = _lib.sinkattn_kv_copy(k_pages.data_ptr(), v_pages.data_ptr(), copies.data_ptr(), ctypes.byref(dims),
-                               _raw_stream(device))
+    st = _lib.sinkattn_kv_copy(k_pages.data_ptr(), v_pages.data_ptr(), copies.data_ptr(),
+                               MoveDims(L, n, Hkv, D, PS, P, 0, 0), _raw_stream(device))
     if st != OK:
         raise SinkAttnError(st, "sinkattn_kv_copy")
 
@@ -529,18 +540,18 @@ def sinkattn_kv_copy(k_pages, v_pages, copies):
 def sinkattn_kv_compact(k_pages, v_pages, page_table, start_pos, accepted, num_accepted):
     """Moves the accepted drafted tokens together, in place: cache position start_pos[b] + accepted[b][i] to
     start_pos[b] + i for i < num_accepted[b].  Pools as in sinkattn_kv_copy; accepted [B, <= 16] int32."""
-    L, P, Hkv, PS, D = _pools(k_pages, v_pages)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(start_pos, "start_pos", torch.int32, 1)
-    _need(accepted, "accepted", torch.int32, 2)
-    _need(num_accepted, "num_accepted", torch.int32, 1)
-    B, A = accepted.shape
-    if page_table.shape[0] != B or start_pos.shape[0] != B or num_accepted.shape[0] != B:
+    device = torch._C._cuda_getDevice()
+    L, P, Hkv, PS, D = _pools(k_pages, v_pages, device)
+    _arg(page_table, "page_table", _i32, 2, device)
+    _arg(start_pos, "start_pos", _i32, 1, device)
+    _arg(accepted, "accepted", _i32, 2, device)
+    _arg(num_accepted, "num_accepted", _i32, 1, device)
+    (B, A), (rows, mp) = accepted.shape, page_table.shape
+    if rows != B or start_pos.shape[0] != B or num_accepted.shape[0] != B:
         raise ValueError("inconsistent compact shapes")
-    device = _here(k_pages, v_pages, page_table, start_pos, accepted, num_accepted)
-    dims = MoveDims(L, B, Hkv, D, PS, P, page_table.shape[1], A)
     st = _lib.sinkattn_kv_compact(k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), start_pos.data_ptr(),
-                                  accepted.data_ptr(), num_accepted.data_ptr(), ctypes.byref(dims), _raw_stream(device))
+                                  accepted.data_ptr(), num_accepted.data_ptr(), MoveDims(L, B, Hkv, D, PS, P, mp, A),
+                                  _raw_stream(device))
     if st != OK:
         raise SinkAttnError(st, "sinkattn_kv_compact")
 
@@ -562,30 +573,32 @@ def sinkattn_decode_beams(q, k_pages, v_pages, page_table, kv_lens, sinks, scale
 
     q [N, K, Hq, 64]; page_table [N, K, max_pages]; kv_lens [N, K].  Returns (out [N, K, Hq, 64], lse [N, K, Hq]).
     """
-    _need(q, "q", torch.bfloat16, 4)
-    _need(k_pages, "k_pages", torch.bfloat16, 4)
-    _need(v_pages, "v_pages", torch.bfloat16, 4)
-    _need(page_table, "page_table", torch.int32, 3)
-    _need(kv_lens, "kv_lens", torch.int32, 2)
-    _need(sinks, "sinks", torch.float32, 1)
-    if v_pages.shape != k_pages.shape:
+    device = torch._C._cuda_getDevice()
+    _arg(q, "q", _bf16, 4, device)
+    _arg(k_pages, "k_pages", _bf16, 4, device)
+    _arg(v_pages, "v_pages", _bf16, 4, device)
+    _arg(page_table, "page_table", _i32, 3, device)
+    _arg(kv_lens, "kv_lens", _i32, 2, device)
+    _arg(sinks, "sinks", _f32, 1, device)
+    P, Hkv, PS, _ = pool = k_pages.shape
+    if v_pages.shape != pool:
         raise ValueError("k_pages and v_pages must have the same shape")
-    N, K, Hq, D = q.shape
-    if page_table.shape[:2] != (N, K) or kv_lens.shape != (N, K) or sinks.shape[0] != Hq:
+    N, K, Hq, D = shape = q.shape
+    rows, beams, mp = page_table.shape
+    if rows != N or beams != K or kv_lens.shape != shape[:2] or sinks.shape[0] != Hq:
         raise ValueError("inconsistent decode_beams shapes")
-    device = _here(q, k_pages, v_pages, page_table, kv_lens, sinks)
-    dims = beams_dims(q, k_pages, page_table, num_workers)
-    ref = ctypes.byref(dims)
-    nbytes = _lib.sinkattn_decode_beams_workspace_size(ref)
+    dims = BeamsDims(N, K, Hq, Hkv, D, PS, P, mp, num_workers)
+    nbytes = _lib.sinkattn_decode_beams_workspace_size(dims)
+    scale = float(scale)
     if nbytes == 0:  # invalid dims: the call says why
-        st = _lib.sinkattn_decode_beams(None, None, None, None, None, None, float(scale), None, None, ref, None, 0, None)
+        st = _lib.sinkattn_decode_beams(None, None, None, None, None, None, scale, None, None, dims, None, 0, None)
         raise SinkAttnError(st if st != OK else ERR_CUDA, "sinkattn_decode_beams")
-    out = _out(out, "out", torch.bfloat16, (N, K, Hq, D), q)
+    out = _out(out, "out", _bf16, shape, q, device)
     if lse is not None or return_lse:
-        lse = _out(lse, "lse", torch.float32, (N, K, Hq), q)
-    workspace, nbytes = _room(workspace, nbytes, q)
+        lse = _out(lse, "lse", _f32, (N, K, Hq), q, device)
+    workspace, nbytes = _room(workspace, nbytes, q, device)
     st = _lib.sinkattn_decode_beams(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-                                    kv_lens.data_ptr(), sinks.data_ptr(), float(scale), out.data_ptr(), _at(lse), ref,
+                                    kv_lens.data_ptr(), sinks.data_ptr(), scale, out.data_ptr(), _at(lse), dims,
                                     workspace.data_ptr(), nbytes, _raw_stream(device))
     if st != OK:
         raise SinkAttnError(st, "sinkattn_decode_beams")
