@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
         const unsigned long long key = i < n ? list[i] : 0ull;
         const int r = (int)(rank_of<8>(list, n, key, lane & 7) & 0xffffu);
         if (i < n && r < M) sm.sel[r] = (int)~(unsigned)key;
+        if (i < n && r == M - 1) sm.threshold = key;  // M tokens are at least this group's best
     }
     if (adds) {
         sum = warp_sum(sum, 32);
@@ -453,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     __syncthreads();
 
     // ---- 4. the tokens of the best groups that can be among the M best, ranked
-    const unsigned thr_v = (unsigned)(thr >> 32);
+    const unsigned thr_v = (unsigned)(sm.threshold >> 32);
     for (int i = tid; i < min(n, M) * kGroup; i += kThreads) {
         const int e = sm.sel[i / kGroup] * kGroup + i % kGroup;
         if (e >= sh.len) continue;
@@ -463,7 +464,33 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
             tokens[atomicAdd(&sm.found[1], 1)] = ((unsigned long long)o << 32) | (unsigned)~(e0 + e);
     }
     __syncthreads();
-    const int nt = sm.found[1];
+    int nt = sm.found[1];
+    if (nt > kThreads) {
+        // few groups, or many equal values: the M-th best of the quads' best tokens is a threshold again
+        constexpr int kHeld = kBeamMaxSelect * kGroup / kThreads;
+        unsigned long long held[kHeld], best = 0;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            held[i] = tid + i * kThreads < nt ? tokens[tid + i * kThreads] : 0ull;
+            best = held[i] > best ? held[i] : best;
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            const unsigned long long y = __shfl_xor_sync(0xffffffffu, best, o);
+            best = y > best ? y : best;
+        }
+        if ((lane & 3) == 0) sm.top[tid >> 2] = best;  // every quad has one
+        if (tid == 0) sm.found[1] = 0;
+        __syncthreads();
+        if ((rank_of<4>(sm.top, kQuads, best, lane & 3) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = best;
+        __syncthreads();
+        const unsigned long long least = sm.threshold;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i)
+            if (held[i] && held[i] >= least) tokens[atomicAdd(&sm.found[1], 1)] = held[i];
+        __syncthreads();
+        nt = sm.found[1];
+    }
     unsigned long long* out = a.best + (size_t)blockIdx.x * M;
     for (int i0 = 0; i0 < nt; i0 += kThreads / 8) {
         const int i = i0 + (tid >> 3);
@@ -525,7 +552,7 @@ inline size_t merge_smem(int total) { return sizeof(MergeSmem) + (size_t)((total
 __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a) {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, n = blockIdx.x;
     const int K = a.K, M = a.M, parts = a.parts, per_row = parts * M, total = K * per_row;
     unsigned long long* score = reinterpret_cast<unsigned long long*>(&sm + 1);
     unsigned long long* at = score + ((total + 1) & ~1);
@@ -543,59 +570,61 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < total ? __ldcg(&best[tid + j * kThreads]) : 0ull;
 
-    // ---- 1. each row's log-sum-exp from its shares: a warp per row, a lane per share
-    for (int k = warp; k < K; k += kThreads / 32) {
-        const long long row = (long long)n * K + k;
+    // ---- 1. each row's log-sum-exp from its shares: 8, 16 or 32 lanes a row, a lane per share
+    const int lanes = parts <= 8 ? 8 : (parts <= 16 ? 16 : 32), sub = tid & (lanes - 1);
+    for (int k0 = 0; k0 < K; k0 += kThreads / lanes) {  // whole warps: what is found of a row is in all its lanes
+        const int k = k0 + tid / lanes, there = k < K ? parts : 0;
+        const long long row = (long long)n * K + (k < K ? k : 0);
         const float c = __ldcg(&a.scores[row]);
         const bool done = a.finished && __ldcg(&a.finished[row]);
-        const BeamPart* p = a.part + row * parts;
-        const float4 own = lane < parts ? __ldcg(reinterpret_cast<const float4*>(p + lane)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        auto get = [&](int i) { return i == lane ? own : __ldcg(reinterpret_cast<const float4*>(p + i)); };
+        const float4* p = reinterpret_cast<const float4*>(a.part + row * parts);
+        const float4 own = sub < there ? __ldcg(p + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto get = [&](int i) { return i == sub ? own : __ldcg(p + i); };
+        float m = kNegInf, r = -1e9f, flags = 0.f;  // flags: 1 far out, 2 NaN
+        for (int i = sub; i < there; i += lanes) {
+            const float4 x = get(i);
+            m = fmaxf(m, x.y);
+            r = x.x == kInf ? r : fmaxf(r, x.x);
+            flags = fmaxf(flags, x.z != x.z ? 2.f : (x.x == kInf ? 1.f : 0.f));
+        }
+        for (int o = 1; o < lanes; o <<= 1) {
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, o));
+            flags = fmaxf(flags, __shfl_xor_sync(0xffffffffu, flags, o));
+        }
+        Two sum = {0.f, 0.f};
+        for (int i = sub; i < there; i += lanes) {
+            const float4 x = get(i);
+            const float f = pow2_down(x.x - r);
+            sum = add(sum, Two{x.z * f, x.w * f});
+        }
+        sum = warp_sum(sum, lanes);
         int st = c > kNegInf && c < kInf ? (done ? 2 : 1) : 0;
-        bool bad = c != c || c == kInf;
+        bool bad = k < K && (c != c || c == kInf);
         Two l = {0.f, 0.f};
         if (st == 1) {
-            float m = kNegInf, r = -1e9f;
-            bool far = false, nan = false;
-            for (int i = lane; i < parts; i += 32) {
-                const float4 x = get(i);
-                m = fmaxf(m, x.y);
-                far = far || x.x == kInf;
-                r = x.x == kInf ? r : fmaxf(r, x.x);
-                nan = nan || x.z != x.z;
-            }
-            m = warp_max(m);
-            r = warp_max(r);
-            far = __any_sync(0xffffffffu, far);
-            nan = __any_sync(0xffffffffu, nan);
-            if (nan || m == kInf) {
-                bad = true;
+            if (flags == 2.f || m == kInf) {
+                bad = k < K;
                 st = 0;
             } else if (m == kNegInf) {  // every token is masked
                 st = 0;
-            } else if (!far) {
-                Two sum = {0.f, 0.f};
-                for (int i = lane; i < parts; i += 32) {
-                    const float4 x = get(i);
-                    const float f = pow2_down(x.x - r);
-                    sum = add(sum, Two{x.z * f, x.w * f});
-                }
-                l = natural_log(r, warp_sum(sum, parts));
-            } else {  // shares far out: in 64 bits
-                double sum = 0.0;
-                for (int i = lane; i < parts; i += 32) {
-                    const float4 x = get(i);
-                    if (x.y == kNegInf) continue;
-                    const double s = (double)x.z + (double)x.w;
-                    const double li = x.x == kInf ? (double)x.y + log(s) : ((double)x.x + log2(s)) / (double)kL;
-                    sum += exp(li - (double)m);
-                }
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                l = to_two((double)m + log(sum));
+            } else {
+                l = natural_log(r, sum);
             }
         }
-        if (lane == 0) {
+        if (__any_sync(0xffffffffu, flags == 1.f && st == 1)) {  // shares far out: in 64 bits
+            double d = 0.0;
+            for (int i = sub; i < there; i += lanes) {
+                const float4 x = get(i);
+                if (x.y == kNegInf) continue;
+                const double s = (double)x.z + (double)x.w;
+                const double li = x.x == kInf ? (double)x.y + log(s) : ((double)x.x + log2(s)) / (double)kL;
+                d += exp(li - (double)m);
+            }
+            for (int o = 1; o < lanes; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (flags == 1.f && st == 1) l = to_two((double)m + log(d));
+        }
+        if (sub == 0 && k < K) {
             if (bad) atomicOr(a.err, kErrBadValue);
             sm.lse[k] = l;
             sm.cum[k] = c;
