@@ -290,6 +290,24 @@ def test_refusals(S):
     assert e.value.status == S.ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("V,M", [(300, 20), (1125, 20), (1125, 64), (2047, 64), (2048, 63), (2100, 64), (4232, 24)])
+@pytest.mark.parametrize("fill", ["random", "levels", "equal"])
+def test_few_groups(S, V, M, fill):
+    """Short rows, where the picks reach into most groups of tokens: hundreds of candidates a row, or equal ones."""
+    z, c = make(3, 4, V, torch.bfloat16, seed=V + M)
+    if fill == "levels":  # four values only: ties everywhere
+        z = (z * 0.4).round().clamp(-2, 1)
+    elif fill == "equal":
+        z = torch.full_like(z, 0.25)
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    check(got, reference(z, c, M))
+    if fill == "equal":  # the first tokens of the best beam
+        best = c.argmax(1)
+        assert torch.equal(got[1].long(), (torch.arange(3, device="cuda") * 4 + best)[:, None].expand(3, M))
+        assert torch.equal(got[2].long(), torch.arange(M, device="cuda").expand(3, M))
+
+
 def test_scores_in_place(S):
     """The running scores of the next step over those of this one."""
     z, c = make(70, 6, 9001, torch.bfloat16, seed=23)
