@@ -14,7 +14,7 @@
 //   Best tokens.  The row is cut into groups of 32 consecutive tokens whose maxima stay in shared memory.  The M
 //   best tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there
 //   are M tokens ahead.  So the pass over the row has no list to maintain; afterwards the M-th best of the
-//   64 maxima that quads of threads have met is a threshold, the groups at or above it (M or a few more) are
+//   maxima that teams of threads have met is a threshold, the groups at or above it (M or a few more) are
 //   ranked by counting, and the 32 M tokens of the M best are read again and ranked the same way.  Keys are
 //   (order of the value, ~position), all different, so ties need no case of their own.
 //
@@ -22,7 +22,7 @@
 // bound by HBM (one read of the logits) with the exponentials close behind (one MUFU operation per logit);
 // select_merge_kernel, one CTA per group, launched as its programmatic dependent.
 //
-// Measured (GB300, calls back to back from a graph): 64 groups of 8 rows of 200000 bf16 logits 44.6 us, 4.6 TB/s = 68% of
+// Measured (GB300, calls back to back from a graph): 64 groups of 8 rows of 200000 bf16 logits 42.8 us, 4.8 TB/s = 70% of
 // the copy rate: the pass over the rows takes 29 us (7 TB/s), its tail (threshold, 64 x 32 tokens read again and ranked)
 // 5 us, the merge 3.5, the rest is starts.  32 groups of 8 rows of 50021 f32 logits 20 us (51 MB: 7.5 us of reading); one
 // group of 4 rows of 32000 7.3 us, all latency.  Five or six CTAs an SM (fewer registers, spills) and more, smaller shares
@@ -38,8 +38,11 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnit = 16;             // consecutive tokens that a thread takes at a time: 32 or 64 bytes
 constexpr int kGroup = 2 * kUnit;     // tokens of a group, held by two neighbouring threads
-constexpr int kQuads = kThreads / 4;  // quads of threads; each quad's best group enters the threshold
-static_assert(kQuads >= kBeamMaxSelect, "the threshold needs M maxima");
+// The M-th best of what teams of threads have met is a threshold: 64 teams of four for up to 32 picks, else 128 of two (as
+// many teams as picks would leave several hundred above it).
+constexpr int kMaxTeams = kThreads / 2;
+static_assert(kThreads / 4 >= 2 * 32 && kMaxTeams >= 2 * kBeamMaxSelect, "twice as many teams as picks");
+__device__ __forceinline__ int team_of(int M) { return M > 32 ? 2 : 4; }
 constexpr float kL = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_huge_valf();
 constexpr float kInf = __builtin_huge_valf();
@@ -65,6 +68,8 @@ template <>
 struct Elem<kDtF32> {
     using T = float;
     static constexpr unsigned kNone = 0xFF800000u;  // -inf
+    __device__ static T put(float x) { return x; }  // a value of the type as T, exact
+    __device__ static float at(T x) { return x; }
     __device__ static float get(const T* p) { return __ldcg(p); }
     __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
@@ -75,6 +80,8 @@ template <>
 struct Elem<kDtBf16> {
     using T = unsigned short;
     static constexpr unsigned kNone = 0xFF80u;
+    __device__ static T put(float x) { return (T)(__float_as_uint(x) >> 16); }
+    __device__ static float at(T x) { return __uint_as_float((unsigned)x << 16); }
     __device__ static float get(const T* p) { return __uint_as_float((unsigned)__ldcg(p) << 16); }
     __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
@@ -88,6 +95,8 @@ template <>
 struct Elem<kDtF16> {
     using T = unsigned short;
     static constexpr unsigned kNone = 0xFC00u;
+    __device__ static T put(float x) { return __half_as_ushort(__float2half_rn(x)); }
+    __device__ static float at(T x) { return __half2float(__ushort_as_half(x)); }
     __device__ static float get(const T* p) { return __half2float(__ushort_as_half(__ldcg(p))); }
     __device__ static void unpack(const uint32_t* w, float (&x)[16]) {
 #pragma unroll
@@ -238,6 +247,18 @@ __device__ __forceinline__ unsigned rank_of(const unsigned long long* keys, int 
     return r;
 }
 
+// The best of a team of `team` neighbouring threads, and the number of teams ahead of this one (low half) and of equal
+// best (high half); top: a word per team, written by one of it.
+__device__ __forceinline__ unsigned long long team_best(unsigned long long v, int team) {
+    unsigned long long y = __shfl_xor_sync(0xffffffffu, v, 1);
+    v = y > v ? y : v;
+    y = __shfl_xor_sync(0xffffffffu, v, 2);
+    return team == 4 && y > v ? y : v;
+}
+__device__ __forceinline__ unsigned team_rank(const unsigned long long* top, unsigned long long key, int team, int lane) {
+    return team == 4 ? rank_of<4>(top, kThreads / 4, key, lane & 3) : rank_of<2>(top, kThreads / 2, key, lane & 1);
+}
+
 // What a thread gathers on its way through a share: sum of 2^(x L - r2), the best group it met and its maximum.
 struct Gather {
     float2 s2[2];
@@ -247,7 +268,7 @@ struct Gather {
 
 // One unit's words: its group's maximum to gmax, its exponentials to the sums.
 template <int DT>
-__device__ __forceinline__ void take(const uint32_t* w, int u, bool store, float* gmax, Gather& t) {
+__device__ __forceinline__ void take(const uint32_t* w, int u, bool store, typename Elem<DT>::T* gmax, Gather& t) {
     float x[kUnit];
     Elem<DT>::unpack(w, x);
     float m4[4];
@@ -255,7 +276,7 @@ __device__ __forceinline__ void take(const uint32_t* w, int u, bool store, float
     for (int i = 0; i < 4; ++i) m4[i] = fmaxf(fmax3(x[4 * i], x[4 * i + 1], x[4 * i + 2]), x[4 * i + 3]);
     float gm = fmaxf(fmax3(m4[0], m4[1], m4[2]), m4[3]);
     gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));  // the other half of the group
-    if (store) gmax[u >> 1] = gm;
+    if (store) gmax[u >> 1] = Elem<DT>::put(gm);
     t.best_g = gm > t.best ? u >> 1 : t.best_g;
     t.best = fmaxf(t.best, gm);
     // sums up to 2^kSlack times the reference's lose nothing, so it moves once or twice a row, not with every new
@@ -276,7 +297,7 @@ __device__ __forceinline__ void take(const uint32_t* w, int u, bool store, float
 
 // One pass over the share.  A group is two neighbouring threads' units.
 template <int DT, bool ALIGNED>
-__device__ __forceinline__ void stream(const Share<DT>& sh, float* gmax, Gather& t) {
+__device__ __forceinline__ void stream(const Share<DT>& sh, typename Elem<DT>::T* gmax, Gather& t) {
     using E = Elem<DT>;
     constexpr int kWords = Share<DT>::kWords, kHeld = kWords + (ALIGNED ? 0 : 8);
     constexpr int kBatch = ALIGNED ? 32 / kWords : (kWords == 16 ? 1 : 2);  // units loaded together
@@ -316,20 +337,23 @@ __device__ __forceinline__ void stream(const Share<DT>& sh, float* gmax, Gather&
 }
 
 struct SelectSmem {
-    alignas(16) unsigned long long top[kQuads];  // the quads' best groups
+    alignas(16) unsigned long long top[kMaxTeams];  // the teams' best groups
     float s[kThreads], r[kThreads];              // the threads' sums and references
     int sel[kBeamMaxSelect];
     unsigned long long threshold;
     int found[2];  // entries of the two lists
 };
-// Behind it: the groups at or above the threshold (M quads' at most), the tokens of the M best, every group's maximum.
+// Behind it: the groups at or above the threshold (M teams' at most), and every group's maximum, in the logits' type, which
+// the tokens of the M best replace.  What is left of the SM's memory is L1, and the loads in flight want it: the 64 x 8
+// rows of 200000 take 52 us with 60 KB of L1 and 42 with 124.
 __host__ __device__ inline int groups_of(int tokens) { return (tokens + kGroup - 1) / kGroup; }
-__host__ __device__ inline int list_cap(int groups, int M) {  // a quad has two of every 2 kQuads groups
-    return M * 2 * ((groups + 2 * kQuads - 1) / (2 * kQuads));
+__host__ __device__ inline int list_cap(int groups, int M) {  // a team has at most two of every kThreads / 2 groups
+    return M * 2 * ((groups + kThreads / 2 - 1) / (kThreads / 2));
 }
-__host__ __device__ inline size_t select_smem(int part_len, int M) {
-    const int groups = groups_of(part_len);
-    return sizeof(SelectSmem) + ((size_t)list_cap(groups, M) + M * kGroup + 2) * 8 + (size_t)((groups + 3) & ~3) * 4;
+inline size_t select_smem(int part_len, int M, int dtype) {
+    const size_t groups = groups_of(part_len), maxima = ((groups + 3) & ~size_t(3)) * (dtype == kDtF32 ? 4 : 2);
+    const size_t tokens = (size_t)M * kGroup * 8;
+    return sizeof(SelectSmem) + (size_t)list_cap((int)groups, M) * 8 + (maxima > tokens ? maxima : tokens);
 }
 
 template <int DT>
@@ -358,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     const int groups = groups_of(sh.len);
     unsigned long long* list = reinterpret_cast<unsigned long long*>(&sm + 1);
     unsigned long long* tokens = list + list_cap(groups_of(a.part_len), M);
-    float* gmax = reinterpret_cast<float*>(tokens + M * kGroup + 2);
+    T* gmax = reinterpret_cast<T*>(tokens);
 
     // ---- 1. one pass over the share
     Gather t = {{make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, -1e9f, kNegInf, 0};
@@ -367,21 +391,19 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     sm.s[tid] = (t.s2[0].x + t.s2[0].y) + (t.s2[1].x + t.s2[1].y);
     sm.r[tid] = t.r2;
     unsigned long long top = t.best > kNegInf ? ((unsigned long long)ord32(t.best) << 32) | (unsigned)~t.best_g : 0ull;
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const unsigned long long y = __shfl_xor_sync(0xffffffffu, top, o);
-        top = y > top ? y : top;
-    }
-    if (top == 0) top = (unsigned long long)(kQuads - 1 - (tid >> 2));  // below every group, and different in every quad
-    if ((lane & 3) == 0) sm.top[tid >> 2] = top;
+    const int team = team_of(M), teams = kThreads / team;
+    top = team_best(top, team);
+    if (top == 0) top = (unsigned long long)(teams - 1 - tid / team);  // below every group, and different in every team
+    if (tid % team == 0) sm.top[tid / team] = top;
     if (tid < 2) sm.found[tid] = 0;
     __syncthreads();
 
     // ---- 2. the share's maximum; its sum again against that maximum where it is far out
     float m_all;
     {
-        const unsigned long long x = sm.top[lane], y = sm.top[lane + 32];
-        const unsigned o = __reduce_max_sync(0xffffffffu, (unsigned)((x > y ? x : y) >> 32));
+        unsigned o = 0;
+        for (int i = lane; i < teams; i += 32) o = max(o, (unsigned)(sm.top[i] >> 32));
+        o = __reduce_max_sync(0xffffffffu, o);
         m_all = o ? unord32(o) : kNegInf;
     }
     const bool far = m_all > kPlainRange || (m_all < -kPlainRange && m_all != kNegInf);
@@ -404,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
         __syncthreads();
     }
 
-    // ---- 3. the threshold: the M-th best of the quads' best groups; meanwhile the last warp adds the sums up
-    if ((rank_of<4>(sm.top, kQuads, top, lane & 3) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = top;  // a quad's four
+    // ---- 3. the threshold: the M-th best of the teams' best groups; meanwhile the last warp adds the sums up
+    if ((team_rank(sm.top, top, team, lane) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = top;  // the whole team
     // the last warp adds the threads' sums up meanwhile, a part of it in each of the next stages
     const bool adds = warp == kThreads / 32 - 1;
     float r_all = kNegInf;
@@ -419,8 +441,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     {
         const float thr_f = (thr >> 32) ? unord32((unsigned)(thr >> 32)) : kNegInf;
         for (int g0 = 4 * tid; g0 < groups; g0 += 4 * kThreads) {
-            const float4 v4 = *reinterpret_cast<const float4*>(gmax + g0);
-            const float v[4] = {v4.x, v4.y, v4.z, v4.w};
+            struct alignas(4 * sizeof(T)) Four {
+                T x[4];
+            };
+            const Four four = *reinterpret_cast<const Four*>(gmax + g0);
+            const float v[4] = {E::at(four.x[0]), E::at(four.x[1]), E::at(four.x[2]), E::at(four.x[3])};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (v[i] >= thr_f && v[i] > kNegInf && g0 + i < groups) {
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
         }
     }
     __syncthreads();
-    const int n = sm.found[0];  // <= M x (groups of a quad)
+    const int n = sm.found[0];  // <= M x (groups of a team)
     for (int i0 = 0; i0 < n; i0 += kThreads / 8) {
         const int i = i0 + (tid >> 3);
         const unsigned long long key = i < n ? list[i] : 0ull;
@@ -466,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     __syncthreads();
     int nt = sm.found[1];
     if (nt > kThreads) {
-        // few groups, or many equal values: the M-th best of the quads' best tokens is a threshold again
+        // few groups, or many equal values: the M-th best of the teams' best tokens is a threshold again
         constexpr int kHeld = kBeamMaxSelect * kGroup / kThreads;
         unsigned long long held[kHeld], best = 0;
 #pragma unroll
@@ -474,15 +499,11 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
             held[i] = tid + i * kThreads < nt ? tokens[tid + i * kThreads] : 0ull;
             best = held[i] > best ? held[i] : best;
         }
-#pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            const unsigned long long y = __shfl_xor_sync(0xffffffffu, best, o);
-            best = y > best ? y : best;
-        }
-        if ((lane & 3) == 0) sm.top[tid >> 2] = best;  // every quad has one
+        best = team_best(best, team);  // every thread has one
+        if (tid % team == 0) sm.top[tid / team] = best;
         if (tid == 0) sm.found[1] = 0;
         __syncthreads();
-        if ((rank_of<4>(sm.top, kQuads, best, lane & 3) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = best;
+        if ((team_rank(sm.top, best, team, lane) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = best;
         __syncthreads();
         const unsigned long long least = sm.threshold;
 #pragma unroll
@@ -539,7 +560,7 @@ __device__ __forceinline__ Two to_two(double x) {
 }
 
 struct MergeSmem {
-    alignas(16) unsigned long long top[kQuads];  // the quads' best scores' orders, 0: none
+    alignas(16) unsigned long long top[kMaxTeams];  // the teams' best scores' orders, 0: none
     Two lse[kBeamMaxBeams];
     float cum[kBeamMaxBeams];
     int state[kBeamMaxBeams];  // 0: no continuation, 1: read, 2: finished
@@ -553,7 +574,7 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     extern __shared__ __align__(16) unsigned char smem_raw[];
     MergeSmem& sm = *reinterpret_cast<MergeSmem*>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, n = blockIdx.x;
-    const int K = a.K, M = a.M, parts = a.parts, per_row = parts * M, total = K * per_row;
+    const int K = a.K, M = a.M, parts = a.parts, shares = K * parts, total = shares * M;
     unsigned long long* score = reinterpret_cast<unsigned long long*>(&sm + 1);
     unsigned long long* at = score + ((total + 1) & ~1);
     unsigned long long* list_score = at + ((total + 1) & ~1);
@@ -566,9 +587,11 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     // hold anything and are not looked at)
     constexpr int kAhead = 4;
     const unsigned long long* best = a.best + (long long)n * total;
+    // candidate i: the shares' best ones, then their second, and so on, which spreads the good ones over the threads
+    auto load = [&](int i) { return __ldcg(&best[i % shares * M + i / shares]); };
     unsigned long long ahead[kAhead];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < total ? __ldcg(&best[tid + j * kThreads]) : 0ull;
+    for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < total ? load(tid + j * kThreads) : 0ull;
 
     // ---- 1. each row's log-sum-exp from its shares: 8, 16 or 32 lanes a row, a lane per share
     const int lanes = parts <= 8 ? 8 : (parts <= 16 ? 16 : 32), sub = tid & (lanes - 1);
@@ -633,7 +656,7 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     }
     __syncthreads();
 
-    // ---- 2. the candidates; the M-th best of the quads' best scores bounds the M-th best of all
+    // ---- 2. the candidates; the M-th best of the teams' best scores bounds the M-th best of all
     unsigned long long mine = 0;
     int j = 0;
 #pragma unroll 1
@@ -643,14 +666,14 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
 #pragma unroll
             for (int q = 1; q < kAhead; ++q) key = j == q ? ahead[q] : key;
         } else {
-            key = __ldcg(&best[i]);
+            key = load(i);
         }
-        const int k = i / per_row, st = sm.state[k];
+        const int share = i % shares, k = share / parts, st = sm.state[k];
         if (st == 1 && key) {
             const Two lse = sm.lse[k], d = two_sum(unord32((unsigned)(key >> 32)), -lse.hi);
             x = ord_two(add(Two{sm.cum[k], 0.f}, Two{d.hi, d.lo - lse.lo}));
             where = ((unsigned long long)k << 32) | ~(unsigned)key;
-        } else if (st == 2 && i == k * per_row) {
+        } else if (st == 2 && i < shares && share == k * parts) {
             x = ord_two(Two{sm.cum[k], 0.f});
             where = ((unsigned long long)k << 32) | (unsigned)a.pad_token;
         }
@@ -658,20 +681,18 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
         at[i] = where;
         mine = x > mine ? x : mine;
     }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        const unsigned long long y = __shfl_xor_sync(0xffffffffu, mine, o);
-        mine = y > mine ? y : mine;
-    }
-    if ((lane & 3) == 0) sm.top[tid >> 2] = mine;
+    const unsigned long long own = mine;
+    const int team = team_of(M);
+    mine = team_best(mine, team);
+    if (tid % team == 0) sm.top[tid / team] = mine;
     __syncthreads();
     {
-        const unsigned r = rank_of<4>(sm.top, kQuads, mine, lane & 3), above = r & 0xffffu, level = r >> 16;
+        const unsigned r = team_rank(sm.top, mine, team, lane), above = r & 0xffffu, level = r >> 16;
         if (above < (unsigned)M && above + level >= (unsigned)M) sm.threshold = mine;  // equal scores write the same
     }
     __syncthreads();
     const unsigned long long thr = sm.threshold;
-    if (mine && mine >= thr) {
+    if (own && own >= thr) {
         for (int i = tid; i < total; i += kThreads) {
             const unsigned long long x = score[i];
             if (x && x >= thr) {
@@ -756,7 +777,7 @@ cudaError_t beam_select_launch(const BeamArgs& a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)units);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = select_smem(a.part_len, a.M);
+    cfg.dynamicSmemBytes = select_smem(a.part_len, a.M, a.dtype);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
