@@ -587,8 +587,14 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     // hold anything and are not looked at)
     constexpr int kAhead = 4;
     const unsigned long long* best = a.best + (long long)n * total;
-    // candidate i: the shares' best ones, then their second, and so on, which spreads the good ones over the threads
-    auto load = [&](int i) { return __ldcg(&best[i % shares * M + i / shares]); };
+    // Which candidate is the i-th, so that the best are spread over the teams (where they meet in a few, the threshold is low).
+    // Few shares: their best ones, then their second and so on (26 groups of 16 rows, 24 picks: 12.5 us, 13.7 share by share).
+    // Many: share by share, which reads in lines (8 groups of 8 rows of four shares: 13.5 us, 14.6 rank by rank).  Many picks:
+    // share by share, each turned by one more than the one before (32 beams, 64 picks: 25 us, 40 rank by rank).
+    const bool by_rank = M <= 32 && parts <= 2;
+    auto share_at = [&](int i) { return by_rank ? i % shares : i / M; };
+    auto rank_at = [&](int i, int share) { return by_rank ? i / shares : (i - share * M + (M > 32 ? share : 0)) % M; };
+    auto load = [&](int i) { return __ldcg(&best[share_at(i) * M + rank_at(i, share_at(i))]); };
     unsigned long long ahead[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) ahead[j] = tid + j * kThreads < total ? load(tid + j * kThreads) : 0ull;
@@ -668,12 +674,12 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
         } else {
             key = load(i);
         }
-        const int share = i % shares, k = share / parts, st = sm.state[k];
+        const int share = share_at(i), k = share / parts, st = sm.state[k];
         if (st == 1 && key) {
             const Two lse = sm.lse[k], d = two_sum(unord32((unsigned)(key >> 32)), -lse.hi);
             x = ord_two(add(Two{sm.cum[k], 0.f}, Two{d.hi, d.lo - lse.lo}));
             where = ((unsigned long long)k << 32) | ~(unsigned)key;
-        } else if (st == 2 && i < shares && share == k * parts) {
+        } else if (st == 2 && share == k * parts && rank_at(i, share) == 0) {
             x = ord_two(Two{sm.cum[k], 0.f});
             where = ((unsigned long long)k << 32) | (unsigned)a.pad_token;
         }
