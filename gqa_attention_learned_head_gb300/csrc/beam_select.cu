@@ -756,12 +756,16 @@ cudaError_t beam_plan(int N, int K, int V, int M, BeamPlan* plan) {
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     const long long rows = (long long)N * K;
-    // shares of a row: as many as run at once (four CTAs an SM), but none below 4096 tokens (one step of a thread)
+    // shares of a row: as many as run at once (four CTAs an SM), but none below 4096 tokens (one step of a thread), and no
+    // more than 512 candidates for the merge (8 groups of 8 rows of 200000, 16 picks: 13.5 us with 512 of them, 18 with 1024),
+    // or 768 where the SMs would not even be half full (5 groups of 12 rows of 143530, 23 picks: 17.3 us, 23.8 with one share a row)
     long long parts = rows > 0 ? (4ll * sms) / rows : 1;
     const long long fine = V / 4096;
     if (parts > fine) parts = fine;
-    const long long least = (V + kBeamMaxPart - 1) / kBeamMaxPart;
-    if (parts > kBeamMaxCands / 8 / ((long long)K * M)) parts = kBeamMaxCands / 8 / ((long long)K * M);
+    const long long least = ((long long)V + kBeamMaxPart - 1) / kBeamMaxPart;
+    long long few = 512 / ((long long)K * M);
+    if (2 * rows * few <= sms) few = 768 / ((long long)K * M);
+    if (parts > few) parts = few;
     if (parts < least) parts = least;
     if (parts < 1) parts = 1;
     const long long len = ((V + parts - 1) / parts + kGroup - 1) / kGroup * kGroup;
