@@ -22,10 +22,10 @@
 // bound by HBM (one read of the logits) with the exponentials close behind (one MUFU operation per logit);
 // select_merge_kernel, one CTA per group, launched as its programmatic dependent.
 //
-// Measured (GB300, calls back to back from a graph): 64 groups of 8 rows of 200000 bf16 logits 42.8 us, 4.8 TB/s = 70% of
+// Measured (GB300, calls back to back from a graph): 64 groups of 8 rows of 200000 bf16 logits 43 us, 4.8 TB/s = 70% of
 // the copy rate: the pass over the rows takes 29 us (7 TB/s), its tail (threshold, 64 x 32 tokens read again and ranked)
-// 5 us, the merge 3.5, the rest is starts.  32 groups of 8 rows of 50021 f32 logits 20 us (51 MB: 7.5 us of reading); one
-// group of 4 rows of 32000 7.3 us, all latency.  Five or six CTAs an SM (fewer registers, spills) and more, smaller shares
+// 5 us, the merge 3.5, the rest is starts.  32 groups of 8 rows of 50021 f32 logits 18.7 us (51 MB: 7.5 us of reading); one
+// group of 4 rows of 32000 7.9 us, all latency.  Five or six CTAs an SM (fewer registers, spills) and more, smaller shares
 // were slower; 64-bit sums and 128-bit keys in the merge took 19.5 us where pairs of floats take 3.5.
 #include "args_beam.h"
 #include "ptx.cuh"
@@ -108,8 +108,8 @@ struct Elem<kDtF16> {
     }
 };
 
-// 32 bytes from a 32-byte boundary: one whole sector.  The first form leaves no copy in L1, the second does (its
-// neighbour reads the sector too).
+// 32 bytes from a 32-byte boundary, one whole sector, without a copy left in L1 or with one (where a neighbour reads the
+// sector too); 16 bytes from a 16-byte boundary.
 __device__ __forceinline__ void load_sector(const void* p, uint32_t* r) {
     asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -120,6 +120,9 @@ __device__ __forceinline__ void load_shared_sector(const void* p, uint32_t* r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
+__device__ __forceinline__ void load_half(const void* p, uint32_t* r) {
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "l"(p));
+}
 
 // A row's share: where it starts, and which of its units can be read in whole sectors.
 template <int DT>
@@ -127,79 +130,71 @@ struct Share {
     using E = Elem<DT>;
     using T = typename E::T;
     static constexpr int kWords = kUnit * (int)sizeof(T) / 4;  // 32-bit words of a unit
+    // A row that starts at no sector's start is read in pieces of this many bytes, shifted (a unit of 16-bit values is one
+    // sector: in halves it takes 48 bytes instead of 64)
+    static constexpr int kPiece = sizeof(T) == 4 ? 32 : 16;
     const T* p;      // first token of the share
     int len, units;  // tokens, units (the last may be partial)
-    int off;         // bytes from the sector boundary at or below p, the same for every unit
-    int lo, hi;      // units [lo, hi) are whole and the sectors they touch lie inside the tensor
+    int lo, hi;      // units [lo, hi) are whole and the pieces they touch lie inside the tensor
 
     __device__ void set(const T* tensor, const T* tensor_end, const T* first, int n) {
         p = first;
         len = n;
         units = (n + kUnit - 1) / kUnit;
-        off = (int)(reinterpret_cast<uintptr_t>(p) & 31);
         hi = n / kUnit;
         lo = 0;
-        if (off) {  // a unit's sectors then start before it and end behind it, by less than a unit
+        const int off = (int)(reinterpret_cast<uintptr_t>(p) % kPiece);
+        if (off) {  // a unit's pieces then start before it and end behind it, by less than one
             const char* c = reinterpret_cast<const char*>(p) - off;
             if (c < reinterpret_cast<const char*>(tensor)) lo = 1;
-            if (hi > 0 && c + hi * (kWords * 4) + 32 > reinterpret_cast<const char*>(tensor_end)) --hi;
+            if (hi > 0 && c + (size_t)hi * (kWords * 4) + kPiece > reinterpret_cast<const char*>(tensor_end)) --hi;
         }
     }
-    // Unit u's values as words: its sectors, or the sectors around it, shifted; token by token at the tensor's edges
-    // and past the share's end (-inf there).  The thread that holds a token, and so the order of every sum, does
-    // not depend on where the row starts.
-    template <bool ALIGNED>
-    __device__ void load(int u, uint32_t* w) const {
-        const char* c = reinterpret_cast<const char*>(p) - off + (size_t)u * (kWords * 4);
-        if (u >= lo && u < hi) {
-            if constexpr (ALIGNED) {
+    // SHIFT: elements from the piece's boundary at or below p to p, the same for every unit; -1: p is at a sector's start.
+    // What a unit of [lo, hi), at c, lies in; and its values as words from that.  The thread that holds a token, and so
+    // the order of every sum, does not depend on where the row starts.
+    template <int SHIFT>
+    static constexpr int kHeld = kWords + (SHIFT > 0 ? kPiece / 4 : 0);
+    template <int SHIFT>
+    __device__ static void fetch(const char* c, uint32_t* raw) {
+        if constexpr (SHIFT < 0) {
 #pragma unroll
-                for (int i = 0; i < kWords / 8; ++i) load_sector(c + 32 * i, &w[8 * i]);
+            for (int i = 0; i < kWords / 8; ++i) load_sector(c + 32 * i, raw + 8 * i);
+        } else {
+            c -= SHIFT * (int)sizeof(T);
+#pragma unroll
+            for (int i = 0; i < kHeld<SHIFT> * 4 / kPiece; ++i) {
+                if constexpr (kPiece == 32) load_shared_sector(c + 32 * i, raw + 8 * i);
+                else load_half(c + 16 * i, raw + 4 * i);
+            }
+        }
+    }
+    __device__ const char* unit(int u) const { return reinterpret_cast<const char*>(p) + (size_t)u * (kWords * 4); }
+    template <int SHIFT>
+    __device__ static void words(const uint32_t* raw, uint32_t* w) {
+        constexpr int kFirst = SHIFT < 0 ? 0 : SHIFT * (int)sizeof(T) / 4;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (SHIFT > 0 && sizeof(T) == 2 && SHIFT % 2 == 1)
+                w[i] = __funnelshift_r(raw[kFirst + i], raw[kFirst + i + 1], 16);
+            else
+                w[i] = raw[kFirst + i];
+        }
+    }
+    // Unit u token by token, -inf behind the share's end: at the tensor's edges.
+    __device__ void tokens(int u, uint32_t* w) const {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                const int e = u * kUnit + i;
+                w[i] = e < len ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(p) + e)) : E::kNone;
             } else {
-#pragma unroll
-                for (int i = 0; i < kWords / 8 + 1; ++i) load_shared_sector(c + 32 * i, &w[8 * i]);
+                const int e = u * kUnit + 2 * i;
+                const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+                const unsigned a = e < len ? (unsigned)__ldcg(h + e) : E::kNone;
+                const unsigned b = e + 1 < len ? (unsigned)__ldcg(h + e + 1) : E::kNone;
+                w[i] = a | (b << 16);
             }
-        } else {
-            uint32_t* to = w + (ALIGNED ? 0 : 8);  // as if shifted by a whole sector: see settle
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) {
-                if constexpr (sizeof(T) == 4) {
-                    const int e = u * kUnit + i;
-                    to[i] = e < len ? __float_as_uint(__ldcg(reinterpret_cast<const float*>(p) + e)) : E::kNone;
-                } else {
-                    const int e = u * kUnit + 2 * i;
-                    const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
-                    const unsigned a = e < len ? (unsigned)__ldcg(h + e) : E::kNone;
-                    const unsigned b = e + 1 < len ? (unsigned)__ldcg(h + e + 1) : E::kNone;
-                    to[i] = a | (b << 16);
-                }
-            }
-        }
-    }
-    // Moves what load<false> brought to the front: w[0 .. kWords) are the unit's words.
-    __device__ void settle(int u, uint32_t (&w)[kWords + 8]) const {
-        if (u >= lo && u < hi) {
-            if (off & 16) {
-#pragma unroll
-                for (int i = 0; i < kWords + 4; ++i) w[i] = w[i + 4];
-            }
-            if (off & 8) {
-#pragma unroll
-                for (int i = 0; i < kWords + 2; ++i) w[i] = w[i + 2];
-            }
-            if (off & 4) {
-#pragma unroll
-                for (int i = 0; i < kWords + 1; ++i) w[i] = w[i + 1];
-            }
-            if constexpr (sizeof(T) == 2) {
-                if (off & 2) {
-#pragma unroll
-                    for (int i = 0; i < kWords; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i) w[i] = w[i + 8];
         }
     }
 };
@@ -296,43 +291,70 @@ __device__ __forceinline__ void take(const uint32_t* w, int u, bool store, typen
 }
 
 // One pass over the share.  A group is two neighbouring threads' units.
-template <int DT, bool ALIGNED>
+template <int DT, int SHIFT>
 __device__ __forceinline__ void stream(const Share<DT>& sh, typename Elem<DT>::T* gmax, Gather& t) {
-    using E = Elem<DT>;
-    constexpr int kWords = Share<DT>::kWords, kHeld = kWords + (ALIGNED ? 0 : 8);
-    constexpr int kBatch = ALIGNED ? 32 / kWords : (kWords == 16 ? 1 : 2);  // units loaded together
+    using S = Share<DT>;
+    constexpr int kWords = S::kWords, kHeld = S::template kHeld<SHIFT>;
+    constexpr int kBatch = SHIFT < 0 ? 32 / kWords : (kWords == 16 ? 1 : 2);  // units loaded together
     const int tid = threadIdx.x;
     int u0 = tid;
-    if constexpr (ALIGNED) {  // while every unit of the warp's step is whole: no tests
-        const char* c = reinterpret_cast<const char*>(sh.p) + (size_t)tid * (kWords * 4);
-        for (; (u0 | 31) + (kBatch - 1) * kThreads < sh.hi; u0 += kThreads * kBatch, c += kThreads * kBatch * (kWords * 4)) {
+    auto any = [&](int u, uint32_t* w) {  // any unit's words
+        if (u >= sh.lo && u < sh.hi) {
+            uint32_t raw[kHeld];
+            S::template fetch<SHIFT>(sh.unit(u), raw);
+            S::template words<SHIFT>(raw, w);
+        } else if (u < sh.units) {
+            sh.tokens(u, w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) w[i] = kWords == 16 ? Elem<DT>::kNone : Elem<DT>::kNone * 0x10001u;
+        }
+    };
+    auto careful = [&]() {  // a step's units, whichever they are
+        if constexpr (SHIFT < 0) {
             uint32_t w[kBatch][kWords];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
+            for (int b = 0; b < kBatch; ++b) any(u0 + b * kThreads, w[b]);
 #pragma unroll
-                for (int i = 0; i < kWords / 8; ++i) load_sector(c + b * kThreads * (kWords * 4) + 32 * i, &w[b][8 * i]);
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) take<DT>(w[b], u0 + b * kThreads, !(tid & 1), gmax, t);
-        }
-    }
-    for (; u0 - (tid & 31) < sh.units; u0 += kThreads * kBatch) {  // whole warps
-        uint32_t w[kBatch][kHeld];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int u = u0 + b * kThreads;
-            if (u < sh.units) {
-                sh.template load<ALIGNED>(u, w[b]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < kHeld; ++i) w[b][i] = sizeof(typename E::T) == 4 ? E::kNone : E::kNone * 0x10001u;
+            for (int b = 0; b < kBatch; ++b) {
+                const int u = u0 + b * kThreads;
+                take<DT>(w[b], u, !(tid & 1) && u < sh.units, gmax, t);
+            }
+        } else {  // one at a time: the many shifted loops' code stays small
+#pragma unroll 1
+            for (int u = u0; u < u0 + kBatch * kThreads && u - (tid & 31) < sh.units; u += kThreads) {
+                uint32_t w[kWords];
+                any(u, w);
+                take<DT>(w, u, !(tid & 1) && u < sh.units, gmax, t);
             }
         }
+    };
+    if (sh.lo) {
+        careful();
+        u0 += kThreads * kBatch;
+    }
+    const char* c = sh.unit(u0);
+    // while the warps' units are whole: no tests
+    for (; (u0 | 31) + (kBatch - 1) * kThreads < sh.hi; u0 += kThreads * kBatch, c += kThreads * kBatch * (kWords * 4)) {
+        uint32_t raw[kBatch][kHeld];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) S::template fetch<SHIFT>(c + b * kThreads * (kWords * 4), raw[b]);
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int u = u0 + b * kThreads;
-            if constexpr (!ALIGNED) sh.settle(u, w[b]);
-            take<DT>(w[b], u, !(tid & 1) && u < sh.units, gmax, t);
+            uint32_t w[kWords];
+            S::template words<SHIFT>(raw[b], w);
+            take<DT>(w, u0 + b * kThreads, !(tid & 1), gmax, t);
         }
+    }
+    for (; u0 - (tid & 31) < sh.units; u0 += kThreads * kBatch) careful();
+}
+// The same for where the share starts, which is known only now: one loop for each of the places that a row may start at (64 x
+// 8 rows of 200001 bf16: 49 us; with the shift chosen at run time 60).
+template <int DT, int SHIFT = 0>
+__device__ __forceinline__ void stream_from(int shift, const Share<DT>& sh, typename Elem<DT>::T* gmax, Gather& t) {
+    if constexpr (SHIFT < Share<DT>::kPiece / (int)sizeof(typename Elem<DT>::T)) {
+        if (shift == SHIFT) stream<DT, SHIFT>(sh, gmax, t);
+        else stream_from<DT, SHIFT + 1>(shift, sh, gmax, t);
     }
 }
 
@@ -386,8 +408,9 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
 
     // ---- 1. one pass over the share
     Gather t = {{make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, -1e9f, kNegInf, 0};
-    if (sh.off == 0) stream<DT, true>(sh, gmax, t);
-    else stream<DT, false>(sh, gmax, t);
+    const unsigned start = (unsigned)reinterpret_cast<uintptr_t>(sh.p);
+    if (start % 32 == 0) stream<DT, -1>(sh, gmax, t);
+    else stream_from<DT>((int)(start % Share<DT>::kPiece / sizeof(T)), sh, gmax, t);
     sm.s[tid] = (t.s2[0].x + t.s2[0].y) + (t.s2[1].x + t.s2[1].y);
     sm.r[tid] = t.r2;
     unsigned long long top = t.best > kNegInf ? ((unsigned long long)ord32(t.best) << 32) | (unsigned)~t.best_g : 0ull;
@@ -410,14 +433,9 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     if (far) {
         float sum = 0.f;
         for (int u = tid; u < sh.units; u += kThreads) {
-            uint32_t w[kWords + 8];
+            uint32_t w[kWords];
             float x[kUnit];
-            if (sh.off == 0) {
-                sh.template load<true>(u, w);
-            } else {
-                sh.template load<false>(u, w);
-                sh.settle(u, w);
-            }
+            sh.tokens(u, w);
             E::unpack(w, x);
 #pragma unroll
             for (int i = 0; i < kUnit; ++i) sum += fast_exp2((x[i] - m_all) * kL);
