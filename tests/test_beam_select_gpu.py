@@ -308,6 +308,25 @@ def test_few_groups(S, V, M, fill):
         assert torch.equal(got[2].long(), torch.arange(M, device="cuda").expand(3, M))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V,M", [(40009, 64), (777, 64), (33, 64)])
+def test_every_start_of_a_row(S, dtype, V, M):
+    """One row's logits 32 times, at every distance from a sector's start: the same scores to the last bit, so that the
+    beams come in their order at every token."""
+    z, _ = make(1, 1, V, dtype, seed=V)
+    stride = V + 1 + V % 2  # odd
+    buf = torch.full((32 * stride,), 50.0, dtype=dtype, device="cuda")
+    rows = buf.as_strided((1, 32, V), (32 * stride, stride, 1))
+    rows.copy_(z.expand(1, 32, V))
+    c = torch.full((1, 32), -3.0, device="cuda")
+    got = S.sinkattn_beam_select(rows, c, M)
+    assert S.sinkattn_get_error() == 0
+    assert torch.equal(got[1][0].long(), torch.arange(M, device="cuda") % 32)
+    order = torch.sort(z.view(-1).float(), descending=True, stable=True)[1]
+    assert torch.equal(got[2][0].long(), order[:2].repeat_interleave(32))
+    check(got, reference(rows, c, M))
+
+
 def test_scores_in_place(S):
     """The running scores of the next step over those of this one."""
     z, c = make(70, 6, 9001, torch.bfloat16, seed=23)
