@@ -28,6 +28,7 @@
 // group of 4 rows of 32000 7.9 us, all latency.  Five or six CTAs an SM (fewer registers, spills) and more, smaller shares
 // were slower; 64-bit sums and 128-bit keys in the merge took 19.5 us where pairs of floats take 3.5.
 #include "args_beam.h"
+#include "errors_beam.h"
 #include "ptx.cuh"
 
 #include <cuda_fp16.h>

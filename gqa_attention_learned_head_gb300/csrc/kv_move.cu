@@ -10,6 +10,7 @@
 // accepted tokens of 256 requests in 24 layers (214 MB) 32.5 us, 6.6 TB/s = 97%; 256 tails of a page 2.8 us, 32 trees
 // of 8 tokens 2.2 us, both little more than the latency of one kernel.
 #include "args_pages.h"
+#include "errors_beam.h"
 #include "ptx.cuh"
 
 namespace sinkattn {

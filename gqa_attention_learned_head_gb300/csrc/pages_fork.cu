@@ -24,6 +24,7 @@
 // plan and 11.5 in the application; 4 rows of one group 7.3 us.  The simplest form
 // (an atomic for every holder that comes or goes) took 54 us.
 #include "args_pages.h"
+#include "errors_beam.h"
 #include "ptx.cuh"
 
 #include <climits>

@@ -15,9 +15,6 @@ enum : unsigned {
     kErrBadPage = 1u << 4,
     kErrTimeout = 1u << 5,
     kErrBadLength = 1u << 7,
-    kErrNoPages = 1u << 8,
-    kErrBadValue = 1u << 9,
-    kErrBadIndex = 1u << 10,
 };
 
 // A wait polls try_wait at most this many times (each poll may also suspend
