@@ -364,7 +364,8 @@ struct SelectSmem {
     float s[kThreads], r[kThreads];              // the threads' sums and references
     int sel[kBeamMaxSelect];
     unsigned long long threshold;
-    int found[2];  // entries of the two lists
+    int found[3];  // entries of the lists of groups, of tokens and of the tokens that a second threshold leaves: a word
+                   // each, so that none is written again while it may still be read
 };
 // Behind it: the groups at or above the threshold (M teams' at most), and every group's maximum, in the logits' type, which
 // the tokens of the M best replace.  What is left of the SM's memory is L1, and the loads in flight want it: the 64 x 8
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
     top = team_best(top, team);
     if (top == 0) top = (unsigned long long)(teams - 1 - tid / team);  // below every group, and different in every team
     if (tid % team == 0) sm.top[tid / team] = top;
-    if (tid < 2) sm.found[tid] = 0;
+    if (tid < 3) sm.found[tid] = 0;
     __syncthreads();
 
     // ---- 2. the share's maximum; its sum again against that maximum where it is far out
@@ -520,16 +521,15 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
         }
         best = team_best(best, team);  // every thread has one
         if (tid % team == 0) sm.top[tid / team] = best;
-        if (tid == 0) sm.found[1] = 0;
         __syncthreads();
         if ((team_rank(sm.top, best, team, lane) & 0xffffu) == (unsigned)(M - 1)) sm.threshold = best;
         __syncthreads();
         const unsigned long long least = sm.threshold;
 #pragma unroll
         for (int i = 0; i < kHeld; ++i)
-            if (held[i] && held[i] >= least) tokens[atomicAdd(&sm.found[1], 1)] = held[i];
+            if (held[i] && held[i] >= least) tokens[atomicAdd(&sm.found[2], 1)] = held[i];
         __syncthreads();
-        nt = sm.found[1];
+        nt = sm.found[2];
     }
     unsigned long long* out = a.best + (size_t)blockIdx.x * M;
     for (int i0 = 0; i0 < nt; i0 += kThreads / 8) {

@@ -336,3 +336,35 @@ def test_scores_in_place(S):
     assert got[0].data_ptr() == kept.data_ptr()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert S.sinkattn_get_error() == 0
+
+
+def levels(N, K, V, dtype, seed):
+    """Logits of four values (whole-number draws, the same on every machine) and scores that keep the beams apart."""
+    g = torch.Generator().manual_seed(seed)
+    z = (torch.randint(0, 4, (N, K, V), generator=g) - 2).to(dtype)
+    c = -(0.37 * torch.arange(K) + 0.053 * torch.arange(N)[:, None]).float()
+    return z.cuda(), c.cuda()
+
+
+def in_order(z, c, M):
+    """The reference's picks where scores of different beams are so far apart that every pick is certain."""
+    ref = reference(z, c, M + 1 if M < z.shape[1] * z.shape[2] else M)
+    step = -np.diff(ref[0], axis=1)
+    assert np.all((step == 0) | (step > 4 * LSE_TOL))  # equal ones are of one beam: the draw's, not the call's
+    return tuple(x[:, :M] for x in ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,M,fill", [(2100, 64, "levels"), (1125, 40, "levels"), (400, 20, "equal")])
+def test_second_threshold_again_and_again(S, dtype, V, M, fill):
+    """More than 256 equal tokens in the best groups of every row, in every resident block at once: the tokens that the second
+    threshold leaves are the same, and the reference's, each time."""
+    z, c = levels(64, 8, V, dtype, seed=V)
+    if fill == "equal":
+        z = torch.full_like(z, 0.25)
+    first = S.sinkattn_beam_select(z, c, M)
+    check(first, in_order(z, c, M), exact=True)
+    for _ in range(200):
+        again = S.sinkattn_beam_select(z, c, M)
+        assert all(torch.equal(x, y) for x, y in zip(first, again))
+    assert S.sinkattn_get_error() == 0
