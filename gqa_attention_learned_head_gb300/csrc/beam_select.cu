@@ -542,9 +542,23 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const BeamArgs
 }
 
 // ---------------------------------------------------------------------------- merge over a group's rows
-// Order of a score hi + lo as an unsigned number; every score's is above 0.
+// Order of a finite score hi + lo as an unsigned number; every score's is above 0.
 __device__ __forceinline__ unsigned long long ord_two(Two x) {
-    return ((unsigned long long)ord32(x.hi) << 32) | ord32(fabsf(x.hi) < kInf ? x.lo : 0.f);
+    return ((unsigned long long)ord32(x.hi) << 32) | ord32(x.lo);
+}
+// ... and of c + (z - lse), all finite.  Where a sum on the way leaves f32's range (a mask of the type's lowest value on a beam
+// marked by the lowest score) it is taken again in quarters, which stay inside; a score below the range is -inf, after all
+// that are within it and among its like by the quarter as f32 holds it.
+__device__ __forceinline__ unsigned long long ord_score(float c, float z, Two lse) {
+    auto sum = [&](float f) {
+        const Two d = two_sum(f * z, -f * lse.hi);
+        return add(Two{f * c, 0.f}, Two{d.hi, d.lo - f * lse.lo});
+    };
+    const Two x = sum(1.f);
+    if (fabsf(x.hi) < kInf) return ord_two(x);  // neither infinite nor, from two infinities, a NaN
+    const Two q = sum(0.25f);
+    if (fabsf(4.f * q.hi) < kInf) return ord_two(Two{4.f * q.hi, 4.f * q.lo});
+    return ((unsigned long long)ord32(kNegInf) << 32) | ord32(q.hi);
 }
 
 // (r + log2 s) / kL for an integer r, a positive s = hi + lo and kL = L as rounded: to about 2e-9 of the logarithm.
@@ -695,8 +709,7 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
         }
         const int share = share_at(i), k = share / parts, st = sm.state[k];
         if (st == 1 && key) {
-            const Two lse = sm.lse[k], d = two_sum(unord32((unsigned)(key >> 32)), -lse.hi);
-            x = ord_two(add(Two{sm.cum[k], 0.f}, Two{d.hi, d.lo - lse.lo}));
+            x = ord_score(sm.cum[k], unord32((unsigned)(key >> 32)), sm.lse[k]);
             where = ((unsigned long long)k << 32) | ~(unsigned)key;
         } else if (st == 2 && share == k * parts && rank_at(i, share) == 0) {
             x = ord_two(Two{sm.cum[k], 0.f});

@@ -444,8 +444,9 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
  *   workspace  at least sinkattn_beam_select_workspace_size(dims) bytes, 256-byte aligned; it needs no
  *              initialisation and must not be shared by calls that may overlap.
  *
- * A logit of -inf is no continuation.  Where a group has fewer than M, the rest of its row is score -inf,
- * parent -1, token -1.  A beam in use whose score is NaN or +inf, or whose logits hold a NaN or +inf, has
+ * A logit of -inf is no continuation.  A score below f32's range is returned as -inf, after all that are within
+ * it (its beam is out of use in the next step).  Where a group has fewer than M continuations, the rest of its
+ * row is score -inf, parent -1, token -1.  A beam in use whose score is NaN or +inf, or whose logits hold a NaN or +inf, has
  * no continuation and raises SINKATTN_ERR_BAD_VALUE.
  * K * M * ceil(V / 262144) above 4096 (candidates of a group that meet in one block) is
  * SINKATTN_ERR_UNSUPPORTED.

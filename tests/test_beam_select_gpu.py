@@ -9,6 +9,7 @@ order adds nothing.  Together the log-sum-exp is off by at most 5e-6, and a retu
 of its own.  Picks have to be the reference's wherever its next score is further away than twice that.
 """
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -368,3 +369,61 @@ def test_second_threshold_again_and_again(S, dtype, V, M, fill):
         again = S.sinkattn_beam_select(z, c, M)
         assert all(torch.equal(x, y) for x, y in zip(first, again))
     assert S.sinkattn_get_error() == 0
+
+
+def exact_picks(logits, scores, M):
+    """(scores f32, parents, tokens) [N, M] of finite logits and scores from rational numbers, the logarithm alone in 64 bits."""
+    z, c = logits.double().cpu().numpy(), scores.double().cpu().numpy()
+    N, K, V = z.shape
+    out = np.full((N, M), -np.inf, np.float32), np.full((N, M), -1), np.full((N, M), -1)
+    for n in range(N):
+        rows = []
+        for k in range(K):
+            m = z[n, k].max()
+            log = Fraction(float(np.log(np.exp(z[n, k] - m).sum())))
+            rows += [(-(Fraction(c[n, k]) + (Fraction(x) - Fraction(m) - log)), k, v) for v, x in enumerate(z[n, k])]
+        for i, (s, k, v) in enumerate(sorted(rows)[:M]):
+            with np.errstate(over="ignore"):
+                out[0][n, i], out[1][n, i], out[2][n, i] = np.float32(float(-s)), n * K + k, v
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V", [40, 4500])
+def test_scores_below_the_range(S, dtype, V):
+    """Beams marked by the lowest f32 score whose tokens are masked by the type's lowest value: what falls below f32's range is
+    -inf, comes after everything within it, and in its order."""
+    low, masked = torch.finfo(torch.float32).min, torch.finfo(dtype).min
+    K, M = 4, 30
+    z = torch.full((3, K, V), masked, dtype=dtype)
+    ramp = (torch.arange(6) * -0.5).to(dtype)
+    z[0, 0, :6] = ramp                 # six tokens of a beam in use, behind them a beam out of use
+    z[0, 1, 3:9] = ramp
+    z[1, :, 5:11] = ramp               # every beam out of use, two as far down as can be
+    z[2, 0, :4] = ramp[:4]
+    z[2, 1, :] = 0                     # all of the same logit
+    z[2, 2, 7] = 3.0
+    z[2, 3, :2] = ramp[:2]
+    c = torch.tensor([[-1.0, low, low / 2, low], [low, low / 2, low, low / 4], [low / 8, low, low / 2, -3.0]])
+    got = [t.cpu().numpy() for t in S.sinkattn_beam_select(z.cuda(), c.cuda(), M)]
+    assert S.sinkattn_get_error() == 0
+    want = exact_picks(z, c, M)
+    assert not np.isnan(got[0]).any()
+    with np.errstate(invalid="ignore"):
+        assert np.all((got[0] == want[0]) | (np.abs(got[0] - want[0]) <= LSE_TOL + 2.0 ** -23 * np.abs(want[0])))
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[2], want[2])
+
+
+def test_wide_logits_below_the_range(S):
+    """Logits further apart than f32 reaches: z - lse alone falls below the range, and comes back where the score is large."""
+    z = torch.full((2, 1, 50), -3.0e38)
+    z[:, 0, 7] = 3.0e38
+    z[:, 0, 9] = 2.0e38
+    z[:, 0, 20:] = -1.0e38
+    c = torch.tensor([[-2.0], [3.0e38]])
+    got = [t.cpu().numpy() for t in S.sinkattn_beam_select(z.cuda(), c.cuda(), 45)]
+    assert S.sinkattn_get_error() == 0
+    want = exact_picks(z, c, 45)
+    assert np.isneginf(want[0][0]).any() and not np.isneginf(want[0][1]).any()
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[2], want[2])
+    assert np.allclose(got[0], want[0], rtol=2.0 ** -22, atol=LSE_TOL)
