@@ -767,17 +767,26 @@ __global__ void __launch_bounds__(kThreads) select_merge_kernel(const BeamArgs a
     }
 }
 
-// Shared memory that a kernel may be launched with, raised once per device and thread as calls ask for more.
-cudaError_t allow_smem(const void* kernel, int which, size_t bytes) {
-    static thread_local size_t allowed[64][4] = {};
-    if (bytes <= 48 * 1024) return cudaSuccess;
+// Lets the four kernels have the shared memory that any call may ask for, once per device and thread.  The limits belong to the
+// process: every thread sets the same ones, whatever its own call needs, so none is lowered under another's call.
+cudaError_t allow_smem() {
+    static thread_local bool allowed[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && allowed[dev][which] >= bytes) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && dev < 64) allowed[dev][which] = bytes;
-    return e;
+    if (e != cudaSuccess || (dev < 64 && allowed[dev])) return e;
+    auto allow = [](const void* kernel, size_t bytes) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    };
+    constexpr int M = kBeamMaxSelect;
+    const void* rows[3] = {reinterpret_cast<const void*>(select_rows_kernel<kDtF32>),
+                           reinterpret_cast<const void*>(select_rows_kernel<kDtBf16>),
+                           reinterpret_cast<const void*>(select_rows_kernel<kDtF16>)};
+    const int types[3] = {kDtF32, kDtBf16, kDtF16};
+    for (int i = 0; i < 3; ++i)
+        if ((e = allow(rows[i], select_smem(kBeamMaxPart, M, types[i]))) != cudaSuccess) return e;
+    if ((e = allow(reinterpret_cast<const void*>(select_merge_kernel), merge_smem(kBeamMaxCands))) != cudaSuccess) return e;
+    if (dev < 64) allowed[dev] = true;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -826,13 +835,11 @@ cudaError_t beam_select_launch(const BeamArgs& a, cudaStream_t stream) {
     void (*rows)(const BeamArgs) = a.dtype == kDtF32    ? select_rows_kernel<kDtF32>
                                    : a.dtype == kDtBf16 ? select_rows_kernel<kDtBf16>
                                                         : select_rows_kernel<kDtF16>;
-    cudaError_t e = allow_smem(reinterpret_cast<const void*>(rows), a.dtype, cfg.dynamicSmemBytes);
+    cudaError_t e = allow_smem();
     if (e != cudaSuccess) return e;
     if ((e = cudaLaunchKernelEx(&cfg, rows, a)) != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)a.N);
     cfg.dynamicSmemBytes = merge_smem(a.K * a.parts * a.M);
-    if ((e = allow_smem(reinterpret_cast<const void*>(select_merge_kernel), 3, cfg.dynamicSmemBytes)) != cudaSuccess)
-        return e;
     return cudaLaunchKernelEx(&cfg, select_merge_kernel, a);
 }
 

@@ -9,6 +9,7 @@ order adds nothing.  Together the log-sum-exp is off by at most 5e-6, and a retu
 of its own.  Picks have to be the reference's wherever its next score is further away than twice that.
 """
 import math
+from concurrent.futures import ThreadPoolExecutor
 from fractions import Fraction
 
 import numpy as np
@@ -427,3 +428,29 @@ def test_wide_logits_below_the_range(S):
     assert np.isneginf(want[0][0]).any() and not np.isneginf(want[0][1]).any()
     assert np.array_equal(got[1], want[1]) and np.array_equal(got[2], want[2])
     assert np.allclose(got[0], want[0], rtol=2.0 ** -22, atol=LSE_TOL)
+
+
+@pytest.mark.parametrize("shape,large,small", [((40, 8, 200000), 64, 32), ((3, 32, 257), 64, 48)])
+def test_two_host_threads(S, shape, large, small):
+    """A thread's call that needs little shared memory leaves the kernels' limits to another thread's that needs much."""
+    z = torch.randn(shape, device="cuda")
+    c = -torch.rand(shape[:2], device="cuda")
+    torch.cuda.synchronize()
+
+    def call(M):
+        stream = torch.cuda.Stream()
+        got = S.sinkattn_beam_select(z, c, M, stream=stream)
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(1) as a, ThreadPoolExecutor(1) as b:
+        first = a.submit(call, large).result()
+        other = b.submit(call, small).result()
+        again = a.submit(call, large).result()
+        both = [x.submit(call, m) for _ in range(20) for x, m in ((a, large), (b, small))]
+        both = [x.result() for x in both]
+    for x, y, o in zip(first, again, other):
+        assert torch.equal(x, y) and torch.equal(x[:, :small], o)
+    for got, want in zip(both, [first, other] * 20):
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    assert S.sinkattn_get_error() == 0
