@@ -580,12 +580,12 @@ def sinkattn_decode_beams(q, k_pages, v_pages, page_table, kv_lens, sinks, scale
     _arg(page_table, "page_table", _i32, 3, device)
     _arg(kv_lens, "kv_lens", _i32, 2, device)
     _arg(sinks, "sinks", _f32, 1, device)
-    P, Hkv, PS, _ = pool = k_pages.shape
+    P, Hkv, PS, Dk = pool = k_pages.shape
     if v_pages.shape != pool:
         raise ValueError("k_pages and v_pages must have the same shape")
     N, K, Hq, D = shape = q.shape
     rows, beams, mp = page_table.shape
-    if rows != N or beams != K or kv_lens.shape != shape[:2] or sinks.shape[0] != Hq:
+    if rows != N or beams != K or kv_lens.shape != shape[:2] or sinks.shape[0] != Hq or Dk != D:
         raise ValueError("inconsistent decode_beams shapes")
     dims = BeamsDims(N, K, Hq, Hkv, D, PS, P, mp, num_workers)
     nbytes = _lib.sinkattn_decode_beams_workspace_size(dims)

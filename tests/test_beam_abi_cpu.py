@@ -160,3 +160,23 @@ def test_beam_validation_under_sanitizers():
                        capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-2000:] + r.stderr[-4000:]
     assert "AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-4000:]
+
+
+@pytest.mark.parametrize("width", [8, 32, 63, 65, 128])
+def test_pools_of_another_head_size_never_reach_the_library(S, monkeypatch, width):
+    """sinkattn_decode_beams refuses pools whose tokens are not as wide as the queries (CPU tensors, with the test for a GPU
+    left out and a library that must not be called)."""
+    import torch
+
+    class NoLibrary:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} called")
+
+    monkeypatch.setattr(S, "_arg", lambda *a: None)
+    monkeypatch.setattr(S, "_lib", NoLibrary())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    q = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16)
+    pool = torch.zeros(4, 2, 16, width, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        S.sinkattn_decode_beams(q, pool, pool, torch.zeros(1, 2, 3, dtype=torch.int32), torch.zeros(1, 2, dtype=torch.int32),
+                                torch.zeros(16), 0.125)

@@ -289,3 +289,15 @@ def test_refusals(S):
     with pytest.raises(S.SinkAttnError) as e:
         S.sinkattn_decode_beams(*inp, 0.125, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == S.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("width", [8, 32, 63, 65, 128])
+def test_pools_of_another_head_size_are_refused(S, width):
+    """The kernel takes a page as 64 values a token, whatever the pool was made for."""
+    q, k, v, table, lens, sinks = [t.cuda() for t in make(16, 2, [[5, 5]], seed=45)]
+    other = torch.zeros(*k.shape[:3], width, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        S.sinkattn_decode_beams(q, other, other, table, lens, sinks, 0.125)
+    with pytest.raises(ValueError):
+        S.sinkattn_decode_beams(q, k, other, table, lens, sinks, 0.125)
+    assert S.sinkattn_get_error() == 0
