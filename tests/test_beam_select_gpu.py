@@ -454,3 +454,46 @@ def test_two_host_threads(S, shape, large, small):
     for got, want in zip(both, [first, other] * 20):
         assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert S.sinkattn_get_error() == 0
+
+
+def check_picks(got, z, c):
+    """Every pick is another continuation, of the score that it has in 64 bits, and runs of equal scores of one beam are in their
+    tokens' order."""
+    gs, gp, gt = (t.cpu().numpy() for t in got)
+    z, c = z.double().cpu().numpy(), c.double().cpu().numpy()
+    N, K, V = z.shape
+    m = z.max(-1, keepdims=True)
+    score = c[..., None] + (z - m - np.log(np.exp(z - m).sum(-1, keepdims=True)))
+    for n in range(N):
+        live = gp[n] >= 0
+        assert live.sum() == min(gp.shape[1], K * V)
+        k, v, s = gp[n, live] - n * K, gt[n, live], gs[n, live]
+        assert len(set(zip(k.tolist(), v.tolist()))) == live.sum()
+        assert np.all((0 <= k) & (k < K) & (0 <= v) & (v < V))
+        want = score[n, k, v]
+        assert np.all(np.abs(s - want) <= LSE_TOL + 2.0 ** -24 * np.abs(want))
+        assert np.all(np.diff(s) <= 0)
+        same = (np.diff(k) == 0) & (z[n, k[1:], v[1:]] == z[n, k[:-1], v[:-1]])
+        assert np.all(np.diff(v)[same] > 0)
+        for q in range(K):  # no continuation of a beam is left out for a later one of it
+            mine = v[k == q]
+            order = np.lexsort((np.arange(V), -z[n, q]))[:mine.size]
+            assert np.array_equal(mine, order)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("V,M", [(31, 64), (300, 20), (1125, 20), (1125, 64), (2047, 64), (2048, 63), (2100, 64), (4232, 24),
+                                 (40009, 40)])
+@pytest.mark.parametrize("fill", ["random", "levels", "coarse"])
+def test_every_pick(S, dtype, V, M, fill):
+    """Pick by pick, ties among them: flat, coarsely rounded and ordinary logits."""
+    z, c = levels(3, 4, V, dtype, seed=V + M)
+    if fill != "levels":
+        z, _ = make(3, 4, V, dtype, seed=V + M)
+    if fill == "coarse":
+        z = (z * 4).round() / 4
+    got = S.sinkattn_beam_select(z, c, M)
+    assert S.sinkattn_get_error() == 0
+    check_picks(got, z, c)
+    if fill == "levels":
+        check(got, in_order(z, c, M), exact=True)
