@@ -563,7 +563,8 @@ __device__ __forceinline__ unsigned long long ord_score(float c, float z, Two ls
 
 // (r + log2 s) / kL for an integer r, a positive s = hi + lo and kL = L as rounded: to about 2e-9 of the logarithm.
 // s = 2^e m with m in [sqrt(1/2), sqrt(2)), n = m - 1, and the series of ln m = 2 artanh t, t = n / (n + 2), |t| < 0.172,
-// cut behind t^9 / 9 (the next term is below 4e-10); its leading terms carry a second float.
+// cut behind t^9 / 9 (the next term is below 4e-10); its leading terms carry a second float.  The products that a two_sum takes
+// are rounded on their own (__fmul_rn): contracted into its additions they would be counted with two errors.
 __device__ __forceinline__ Two natural_log(float r, Two s) {
     const int b = __float_as_int(s.hi);
     int e = (b >> 23) - 127;
@@ -579,12 +580,12 @@ __device__ __forceinline__ Two natural_log(float r, Two s) {
     p = fmaf(p, q, 1.f / 3.f);
     constexpr float kCh = 2.885390043258667f;          // 2 / ln 2 as two floats
     constexpr float kCl = 3.8519259e-08f;
-    const float ph = kCh * th;
+    const float ph = __fmul_rn(kCh, th);
     const float pl = fmaf(kCh, th, -ph) + (fmaf(kCh, tl, kCl * th) + ph * q * p);
     const Two l2 = add(two_sum(r + (float)e, ph), Two{pl, 0.f});
     constexpr double kInv = 1.0 / (double)kL;          // as two floats
     constexpr float kIh = (float)kInv, kIl = (float)(kInv - (double)kIh);
-    const float h = l2.hi * kIh;
+    const float h = __fmul_rn(l2.hi, kIh);
     return add(Two{h, fmaf(l2.hi, kIh, -h)}, Two{fmaf(l2.hi, kIl, l2.lo * kIh), 0.f});
 }
 __device__ __forceinline__ Two to_two(double x) {

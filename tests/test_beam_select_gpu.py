@@ -9,6 +9,7 @@ order adds nothing.  Together the log-sum-exp is off by at most 5e-6, and a retu
 of its own.  Picks have to be the reference's wherever its next score is further away than twice that.
 """
 import math
+import random
 from concurrent.futures import ThreadPoolExecutor
 from fractions import Fraction
 
@@ -497,3 +498,28 @@ def test_every_pick(S, dtype, V, M, fill):
     check_picks(got, z, c)
     if fill == "levels":
         check(got, in_order(z, c, M), exact=True)
+
+
+def test_logarithm_between_two_beams(S):
+    """Rows of n zeros and nothing else, whose sums are whole numbers: the beams' order hangs on the logarithms alone.
+
+    The logarithm is off by at most 1.6e-9 (series and roundings), and by its base's rounding, 1.34e-8 of the entropy ln n: between
+    two beams 2 x 1.6e-9 + 1.34e-8 x 0.17 = 5.5e-9 here, under half of the 1.2e-8 by which the scores differ at least."""
+    rng, V, N = random.Random(4), 70000, 96
+    z = torch.full((N, 2, V), -math.inf)
+    c, best = torch.empty(N, 2), []
+    while len(best) < N:
+        n0 = int(math.exp(rng.uniform(math.log(20), math.log(60000))))
+        n1 = n0 + rng.randint(-n0 // 7, n0 // 7)
+        c0 = np.float32(rng.uniform(-0.08, -0.01))
+        c1 = np.float32(float(c0) - math.log(n0) + math.log(n1) + rng.uniform(-1e-7, 1e-7))
+        gap = (float(c0) - math.log(n0)) - (float(c1) - math.log(n1))
+        if abs(gap) < 1.2e-8 or abs(math.log(n0 / n1)) > 0.17:
+            continue
+        i = len(best)
+        z[i, 0, :n0], z[i, 1, :n1], c[i, 0], c[i, 1] = 0, 0, float(c0), float(c1)
+        best.append(2 * i + (0 if gap > 0 else 1))
+    s, p, t = S.sinkattn_beam_select(z.cuda(), c.cuda(), 2)
+    assert S.sinkattn_get_error() == 0
+    assert p.cpu().tolist() == [[b, b] for b in best]
+    assert t.cpu().tolist() == [[0, 1]] * N
