@@ -71,6 +71,14 @@ def _need(t, name, dtype, ndim):
         raise ValueError(f"{name} must be a contiguous {ndim}-d tensor, got shape {tuple(t.shape)}")
 
 
+def _pools_match(k_pages, v_pages, head_dim):
+    """Refuses pools of two shapes, or whose tokens are not as wide as the call's queries or keys."""
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have the same shape")
+    if k_pages.shape[3] != head_dim:
+        raise ValueError(f"k_pages must have {head_dim} values a token, got shape {tuple(k_pages.shape)}")
+
+
 def _check(status, what):
     if status != OK:
         raise SinkAttnError(status, what)
@@ -95,9 +103,8 @@ def sinkattn_decode(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
     _need(page_table, "page_table", torch.int32, 2)
     _need(kv_lens, "kv_lens", torch.int32, 1)
     _need(sinks, "sinks", torch.float32, 1)
-    if v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must have the same shape")
     B, Hq, D = q.shape
+    _pools_match(k_pages, v_pages, D)
     if page_table.shape[0] != B or kv_lens.shape[0] != B or sinks.shape[0] != Hq or k_pages.shape[1] == 0:
         raise ValueError("inconsistent decode shapes")
     dims = decode_dims(q, k_pages, page_table, num_workers)
@@ -140,9 +147,8 @@ def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
     _need(page_table, "page_table", torch.int32, 2)
     _need(kv_lens, "kv_lens", torch.int32, 1)
     _need(sinks, "sinks", torch.float32, 1)
-    if v_pages.shape != k_pages.shape:
-        raise ValueError("k_pages and v_pages must have the same shape")
     B, QL, Hq, D = q.shape
+    _pools_match(k_pages, v_pages, D)
     if page_table.shape[0] != B or kv_lens.shape[0] != B or sinks.shape[0] != Hq or k_pages.shape[1] == 0:
         raise ValueError("inconsistent verify shapes")
     dims = verify_dims(q, k_pages, page_table, num_workers)
@@ -176,6 +182,7 @@ def sinkattn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, tree_mask, si
     _need(page_table, "page_table", torch.int32, 2)
     _need(kv_lens, "kv_lens", torch.int32, 1)
     _need(sinks, "sinks", torch.float32, 1)
+    _pools_match(k_pages, v_pages, q.shape[3])
     Hq = q.shape[2]
     dims = verify_dims(q, k_pages, page_table, num_workers)
     if out is None:
@@ -211,6 +218,7 @@ def sinkattn_kv_append(k, v, cu_seqlens, start_pos, page_table, k_pages, v_pages
     _need(v_pages, "v_pages", torch.bfloat16, 4)
     if v.shape != k.shape or v_pages.shape != k_pages.shape or k.shape[1] != k_pages.shape[1]:
         raise ValueError("inconsistent append shapes")
+    _pools_match(k_pages, v_pages, k.shape[2])
     dims = paged_dims(k_pages, page_table, cu_seqlens, k.shape[0], max_seqlen)
     st = _lib.sinkattn_kv_append(_ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(start_pos), _ptr(page_table),
                                  _ptr(k_pages), _ptr(v_pages), ctypes.byref(dims), _stream(stream))
@@ -232,6 +240,7 @@ def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages,
     _need(v_pages, "v_pages", torch.bfloat16, 4)
     T = qkv.shape[0]
     Hkv = k_pages.shape[1]
+    _pools_match(k_pages, v_pages, k_pages.shape[3])  # (the library refuses widths other than 64)
     if qkv.shape[1] != (num_q_heads + 2 * Hkv) * 64 or (bias is not None and bias.shape[0] != qkv.shape[1]):
         raise ValueError("qkv must be [T, (Hq + 2 Hkv) * 64] and bias [(Hq + 2 Hkv) * 64]")
     if q_out is None:
@@ -260,6 +269,7 @@ def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_po
     if max_seqlen is None:
         raise ValueError("max_seqlen is required (an upper bound of the new tokens per sequence)")
     T, Hq, D = q.shape
+    _pools_match(k_pages, v_pages, D)
     dims = paged_dims(k_pages, page_table, cu_seqlens, T, max_seqlen, Hq, share_sms)
     if out is None:
         out = torch.empty_like(q)
@@ -285,7 +295,7 @@ def sinkattn_prefill(q, k, v, cu_seqlens, sinks, scale, causal=True, max_seqlen=
     if max_seqlen is None:
         raise ValueError("max_seqlen is required (an upper bound of the sequence lengths)")
     T, Hq, D = q.shape
-    if k.shape != v.shape or k.shape[0] != T or sinks.shape[0] != Hq:
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D or sinks.shape[0] != Hq:
         raise ValueError("inconsistent prefill shapes")
     dims = PrefillDims(cu_seqlens.shape[0] - 1, T, int(max_seqlen), Hq, k.shape[1], D, int(bool(share_sms)))
     if out is None:
@@ -338,6 +348,7 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
         _need(t, name, dt, nd)
     if lse is not None:
         _need(lse, "lse", torch.float32, 2)
+    _pools_match(k_pages, v_pages, q.shape[2])
     dims = decode_dims(q, k_pages, page_table)
     st = _lib.sinkattn_decode_noalloc(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens),
                                       _ptr(sinks), float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims),

@@ -191,3 +191,34 @@ def test_host_validation_under_sanitizers():
                        text=True, timeout=600)
     assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout[-2000:] + r.stderr[-4000:]
     assert "AddressSanitizer" not in r.stderr and "runtime error" not in r.stderr, r.stderr[-4000:]
+
+
+@pytest.mark.parametrize("width", [8, 32, 65, 128])
+def test_pools_that_do_not_fit_the_queries_never_reach_the_library(S, monkeypatch, width):
+    """Pools whose tokens are not as wide as the queries or keys, or that differ from each other (CPU tensors, with the test
+    for a GPU left out and a library that must not be called)."""
+    import torch
+
+    class NoLibrary:
+        def __getattr__(self, name):
+            raise AssertionError(f"{name} called")
+
+    monkeypatch.setattr(S, "_need", lambda *a: None)
+    monkeypatch.setattr(S, "_lib", NoLibrary())
+    bf, i32 = (lambda *s: torch.zeros(s, dtype=torch.bfloat16)), (lambda *s: torch.zeros(s, dtype=torch.int32))
+    pool, sinks, table, lens, cu = bf(4, 2, 16, 64), torch.zeros(16), i32(3, 2), i32(3), i32(4)
+    wide, few = bf(4, 2, 16, width), bf(3, 2, 16, 64)
+    masks = torch.zeros(3, 2, dtype=torch.int64)
+    for k, v in ((wide, wide), (pool, few), (few, pool)):
+        for call in (lambda: S.sinkattn_decode(bf(3, 16, 64), k, v, table, lens, sinks, 0.125),
+                     lambda: S.sinkattn_decode_noalloc(bf(3, 16, 64), k, v, table, lens, sinks, 0.125, bf(3, 16, 64)),
+                     lambda: S.sinkattn_verify(bf(3, 2, 16, 64), k, v, table, lens, sinks, 0.125),
+                     lambda: S.sinkattn_verify_tree(bf(3, 2, 16, 64), k, v, table, lens, masks, sinks, 0.125),
+                     lambda: S.sinkattn_kv_append(bf(5, 2, 64), bf(5, 2, 64), cu, lens, table, k, v),
+                     lambda: S.sinkattn_prefill_paged(bf(5, 16, 64), k, v, table, cu, lens, sinks, 0.125, max_seqlen=5)):
+            with pytest.raises(ValueError):
+                call()
+    with pytest.raises(ValueError):
+        S.sinkattn_qkv_prologue(bf(5, 20 * 64), None, cu, lens, table, pool, few, 16, 1e4, 32.0, 4096, 32.0, 1.0)
+    with pytest.raises(ValueError):
+        S.sinkattn_prefill(bf(5, 16, 64), bf(5, 2, width), bf(5, 2, width), cu, sinks, 0.125, max_seqlen=5)
