@@ -1,0 +1,110 @@
+"""Calls from several host threads."""
+import threading
+
+import pytest
+import torch
+
+from gqa_attention_learned_head_gb300 import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def S():
+    from gqa_attention_learned_head_gb300 import sinkattn
+
+    return sinkattn
+
+
+def in_new_thread(fn):
+    """What fn returns, or raises, as the first thing that a thread does."""
+    box = []
+
+    def run():
+        try:
+            box.append((fn(), None))
+        except Exception as e:  # noqa: BLE001
+            box.append((None, e))
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    if box[0][1] is not None:
+        raise box[0][1]
+    return box[0][0]
+
+
+def calls(S):
+    """Every entry point with all of its outputs given, by name: (call, its outputs)."""
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    d = W.make_decode(3, 16, 2, [40, 1, 100], seed=1).to("cuda")
+    v = W.make_decode(3, 16, 2, [40, 9, 100], seed=2, q_len=4).to("cuda")
+    p = W.make_prefill(16, 2, [130, 5], seed=3).to("cuda")
+    odd = W.make_prefill(6, 2, [130, 5], seed=4).to("cuda")
+    c = W.make_paged_prefill(16, 2, [5, 30], [20, 7], seed=5).to("cuda")
+    masks = torch.tensor([1, 3, 5, 15], dtype=torch.int64, device="cuda").expand(3, 4).contiguous()
+    like = lambda q: dict(out=torch.zeros_like(q), lse=torch.zeros(q.shape[:-1], device="cuda"))  # noqa: E731
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    out = {n: like(x) for n, x in (("decode", d.q), ("noalloc", d.q), ("verify", v.q), ("tree", v.q), ("prefill", p.q),
+                                   ("prefill odd", odd.q), ("prefill shared", p.q), ("paged", c.q), ("beams", d.q.view(1, 3, 16, 64)))}
+    qkv = torch.randn(27, 20 * 64, device="cuda").to(torch.bfloat16)
+    q_out = torch.zeros(27, 16, 64, dtype=torch.bfloat16, device="cuda")
+    pages = [(c.k_pages.clone(), c.v_pages.clone()) for _ in range(4)]
+    part, part_lse = torch.randn(3, 4, 8, 64, device="cuda"), torch.randn(3, 4, 8, device="cuda")
+    merged = dict(out=torch.zeros(4, 8, 64, dtype=torch.bfloat16, device="cuda"), lse=torch.zeros(4, 8, device="cuda"))
+    z, s = torch.randn(2, 3, 500, device="cuda"), -torch.rand(2, 3, device="cuda")
+    picks = dict(out_scores=torch.zeros(2, 4, device="cuda"), out_parents=i32([[0] * 4] * 2), out_tokens=i32([[0] * 4] * 2))
+    fork = dict(out_table=i32([[0] * 3] * 2), out_lens=i32([0, 0]), out_refs=i32([0] * 6), copies=i32([[0] * 3] * 2))
+    table, held, parents, refs = i32([[0, 1, -1], [2, -1, -1]]), i32([20, 10]), i32([0, 0]), i32([1, 1, 1, 0, 0, 0])
+    dargs = (d.q, d.k_pages, d.v_pages, d.page_table, d.kv_lens, d.sinks, d.scale)
+    vargs = (v.q, v.k_pages, v.v_pages, v.page_table, v.kv_lens)
+    copies, start, acc, num, cargs = i32([[0, 1, 5]]), i32([3, 4]), i32([[1, 2], [0, 3]]), i32([2, 2]), (c.cu_seqlens, c.start_pos)
+    odd_args, p_args = ((x.q, x.k, x.v, x.cu_seqlens, x.sinks, x.scale) for x in (odd, p))
+    return {
+        "decode": (lambda: S.sinkattn_decode(*dargs, workspace=ws, **out["decode"]), out["decode"].values()),
+        "noalloc": (lambda: S.sinkattn_decode_noalloc(*dargs, **out["noalloc"]), out["noalloc"].values()),
+        "verify": (lambda: S.sinkattn_verify(*vargs, v.sinks, v.scale, workspace=ws, **out["verify"]), out["verify"].values()),
+        "tree": (lambda: S.sinkattn_verify_tree(*vargs, masks, v.sinks, v.scale, workspace=ws, **out["tree"]), out["tree"].values()),
+        "prefill": (lambda: S.sinkattn_prefill(*p_args, max_seqlen=130, **out["prefill"]), out["prefill"].values()),
+        "prefill odd": (lambda: S.sinkattn_prefill(*odd_args, max_seqlen=130, **out["prefill odd"]), out["prefill odd"].values()),
+        "prefill shared": (lambda: S.sinkattn_prefill(*p_args, max_seqlen=130, share_sms=True, **out["prefill shared"]),
+                           out["prefill shared"].values()),
+        "paged": (lambda: S.sinkattn_prefill_paged(c.q, c.k_pages, c.v_pages, c.page_table, *cargs, c.sinks, c.scale, max_seqlen=20,
+                                                   **out["paged"]), out["paged"].values()),
+        "append": (lambda: S.sinkattn_kv_append(c.k_new, c.v_new, *cargs, c.page_table, *pages[0], max_seqlen=20), pages[0]),
+        "prologue": (lambda: S.sinkattn_qkv_prologue(qkv, None, *cargs, c.page_table, *pages[1], 16, 1e4, 32.0, 4096, 32.0, 1.0,
+                                                     q_out=q_out), (q_out, *pages[1])),
+        "merge": (lambda: S.sinkattn_merge(part, part_lse, **merged), merged.values()),
+        "select": (lambda: S.sinkattn_beam_select(z, s, 4, workspace=ws, **picks), picks.values()),
+        "fork": (lambda: S.sinkattn_pages_fork(table, held, parents, refs, grow=1, workspace=ws, **fork), fork.values()),
+        "copy": (lambda: S.sinkattn_kv_copy(*pages[2], copies), pages[2]),
+        "compact": (lambda: S.sinkattn_kv_compact(*pages[3], c.page_table, start, acc, num), pages[3]),
+        "beams": (lambda: S.sinkattn_decode_beams(d.q.view(1, 3, 16, 64), d.k_pages, d.v_pages, d.page_table.view(1, 3, -1),
+                                                  d.kv_lens.view(1, 3), d.sinks, d.scale, workspace=ws, **out["beams"]),
+                  out["beams"].values()),
+    }
+
+
+NAMES = ["decode", "noalloc", "verify", "tree", "prefill", "prefill odd", "prefill shared", "paged", "append", "prologue", "merge",
+         "select", "fork", "copy", "compact", "beams"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_first_thing_a_thread_does(S, name):
+    """A host thread whose first use of the GPU is a call: the same outputs as from the main thread."""
+    call, outputs = calls(S)[name]
+    if name == "compact":  # moves tokens: the same start for both
+        outputs = list(outputs)
+        start = [t.clone() for t in outputs]
+    call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in outputs]
+    for i, t in enumerate(outputs):
+        t.copy_(start[i]) if name == "compact" else (t.zero_() if name not in ("append", "prologue", "copy") else None)
+    torch.cuda.synchronize()
+    in_new_thread(call)
+    torch.cuda.synchronize()
+    assert S.sinkattn_get_error() == 0
+    for got, ref in zip(outputs, want):
+        assert torch.equal(got, ref)
+    assert S.sinkattn_get_error() == in_new_thread(S.sinkattn_get_error) == 0
