@@ -84,14 +84,15 @@ def peaks():
 
 # Sources each profiled kernel is compiled from (its own file, the headers it includes).
 KERNEL_SOURCES = {
-    "decode_split_kernel": ["decode.cu", "ptx.cuh", "split_kv.cuh", "args_decode.h", "args_merge.h", "args_common.h"],
+    "decode_split_kernel": ["decode.cu", "ptx.cuh", "smem_limit.h", "split_kv.cuh", "args_decode.h", "args_merge.h",
+                            "args_common.h"],
     "verify_tc_kernel": ["verify_tc.cu", "ptx.cuh", "split_kv.cuh", "tc_tile.cuh", "args_verify.h", "args_merge.h",
                          "args_common.h"],
-    "prefill_pp_kernel": ["prefill_pp.cu", "ptx.cuh", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
+    "prefill_pp_kernel": ["prefill_pp.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
                           "args_common.h"],
-    "prefill_tc_kernel": ["prefill_tc.cu", "ptx.cuh", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
+    "prefill_tc_kernel": ["prefill_tc.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
                           "args_common.h"],
-    "prefill_pp_kernel_paged": ["prefill_pp.cu", "ptx.cuh", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
+    "prefill_pp_kernel_paged": ["prefill_pp.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
                                 "args_common.h"],
     "qkv_prologue_kernel": ["prologue.cu", "ptx.cuh", "args_paged.h", "args_common.h"],
 }

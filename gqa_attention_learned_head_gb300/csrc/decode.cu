@@ -44,6 +44,7 @@
 #include "args_decode.h"
 #include "args_merge.h"
 #include "ptx.cuh"
+#include "smem_limit.h"
 #include "split_kv.cuh"
 
 #ifndef SINKATTN_DECODE_STAGES
@@ -599,15 +600,9 @@ __global__ void __launch_bounds__(kWarps * 32, SINKATTN_DECODE_MIN_BLOCKS)
 }
 
 template <int NT>
-cudaError_t ensure_smem_attr(size_t smem) {
-    static thread_local size_t set_to[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 64 && set_to[dev] >= smem) return cudaSuccess;
-    e = cudaFuncSetAttribute(decode_split_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && dev < 64) set_to[dev] = smem;
-    return e;
+cudaError_t ensure_smem_attr(int dev) {
+    static thread_local bool done[64] = {};
+    return allow_all_smem(reinterpret_cast<const void*>(decode_split_kernel<NT>), dev, done);
 }
 
 }  // namespace
@@ -630,7 +625,7 @@ cudaError_t resident_ctas(int NT, size_t smem, long long* ctas) {
             *ctas = c.ctas;
             return cudaSuccess;
         }
-    e = NT == 1 ? ensure_smem_attr<1>(smem) : ensure_smem_attr<2>(smem);
+    e = NT == 1 ? ensure_smem_attr<1>(dev) : ensure_smem_attr<2>(dev);
     if (e != cudaSuccess) return e;
     int sms = 0, per_sm = 0;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;

@@ -30,6 +30,7 @@
 // the kernel winds down (the other waits then give up too).
 #include "args_prefill.h"
 #include "ptx.cuh"
+#include "smem_limit.h"
 #include "tc_tile.cuh"
 #include "tile_order.cuh"
 
@@ -454,7 +455,7 @@ cudaError_t launch_pp(const PrefillArgs& a, const CUtensorMap& tq, const CUtenso
     const long long grid = tiles_ub * (a.Hq / 2);
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const size_t smem = 1024 + sizeof(Smem) + seq_order_smem_ints(a.N) * sizeof(int);
-    static thread_local size_t set_to[64] = {};
+    static thread_local bool smem_done[64] = {};
     static thread_local int regs_ok[64] = {};  // 0 unknown, 1 checked
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -467,11 +468,7 @@ cudaError_t launch_pp(const PrefillArgs& a, const CUtensorMap& tq, const CUtenso
             return cudaErrorInvalidConfiguration;
         if (dev < 64) regs_ok[dev] = 1;
     }
-    if (dev >= 64 || set_to[dev] < smem) {
-        e = cudaFuncSetAttribute(prefill_pp_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) set_to[dev] = smem;
-    }
+    if ((e = allow_all_smem(reinterpret_cast<const void*>(prefill_pp_kernel<kPaged>), dev, smem_done)) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

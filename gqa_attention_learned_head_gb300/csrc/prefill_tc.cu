@@ -27,6 +27,7 @@
 // Every wait is bounded; a wait that gives up sets the device error word.
 #include "args_prefill.h"
 #include "ptx.cuh"
+#include "smem_limit.h"
 #include "tc_tile.cuh"
 #include "tile_order.cuh"
 
@@ -415,15 +416,11 @@ cudaError_t launch(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMa
     const long long grid = tiles_ub * a.Hq;
     if (grid > 0x7fffffffll) return cudaErrorInvalidConfiguration;
     const size_t smem = 1024 + sizeof(Smem) + seq_order_smem_ints(a.N) * sizeof(int);
-    static thread_local size_t set_to[64] = {};
+    static thread_local bool smem_done[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev >= 64 || set_to[dev] < smem) {
-        e = cudaFuncSetAttribute(prefill_tc_kernel<kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) set_to[dev] = smem;
-    }
+    if ((e = allow_all_smem(reinterpret_cast<const void*>(prefill_tc_kernel<kPaged>), dev, smem_done)) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

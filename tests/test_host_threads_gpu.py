@@ -1,5 +1,6 @@
 """Calls from several host threads."""
 import threading
+from concurrent.futures import ThreadPoolExecutor
 
 import pytest
 import torch
@@ -108,3 +109,42 @@ def test_first_thing_a_thread_does(S, name):
     for got, ref in zip(outputs, want):
         assert torch.equal(got, ref)
     assert S.sinkattn_get_error() == in_new_thread(S.sinkattn_get_error) == 0
+
+
+def decode(S, n, Hq):
+    g = W.make_decode(n, Hq, 2, (1, 40), seed=n).to("cuda")
+    return lambda: S.sinkattn_decode(g.q, g.k_pages, g.v_pages, g.page_table, g.kv_lens, g.sinks, g.scale)
+
+
+def prefill(S, n, Hq):
+    g = W.make_prefill(Hq, 2, (n, 1, 20), seed=n).to("cuda")
+    return lambda: S.sinkattn_prefill(g.q, g.k, g.v, g.cu_seqlens, g.sinks, g.scale, max_seqlen=20)
+
+
+def prefill_paged(S, n, Hq):
+    g = W.make_paged_prefill(Hq, 2, [5] * n, [7] * n, seed=n).to("cuda")
+    return lambda: S.sinkattn_prefill_paged(g.q, g.k_pages, g.v_pages, g.page_table, g.cu_seqlens, g.start_pos, g.sinks,
+                                            g.scale, max_seqlen=7)
+
+
+@pytest.mark.parametrize("Hq", [16, 20, 6])  # 8, 10 and 3 query heads a KV head: the kernels' variants
+@pytest.mark.parametrize("make", [decode, prefill, prefill_paged])
+def test_a_small_batch_leaves_a_large_ones_limits(S, make, Hq):
+    """A kernel's shared memory grows with the batch and its limit belongs to the process."""
+    large, small = make(S, 3000, Hq), make(S, 2, Hq)
+    torch.cuda.synchronize()
+
+    def run(call):
+        got = [t.clone() for t in call()]
+        torch.cuda.synchronize()
+        return got
+
+    with ThreadPoolExecutor(1) as a, ThreadPoolExecutor(1) as b:
+        first = a.submit(run, large).result()
+        other = b.submit(run, small).result()
+        again = a.submit(run, large).result()
+        for x, y in zip(first, again):
+            assert torch.equal(x, y)
+        for x, y in zip(other, b.submit(run, small).result()):
+            assert torch.equal(x, y)
+    assert S.sinkattn_get_error() == 0
