@@ -62,6 +62,18 @@ def _raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _on_stream(fn):
+    """Runs a call with its ``stream`` argument current, so that what it allocates (outputs, workspace) belongs to the
+    stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 def _need(t, name, dtype, ndim):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -94,6 +106,7 @@ def sinkattn_decode_workspace_size(q, k_pages, page_table, num_workers=0) -> int
     return int(_lib.sinkattn_decode_workspace_size(ctypes.byref(decode_dims(q, k_pages, page_table, num_workers))))
 
 
+@_on_stream
 def sinkattn_decode(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=None, lse=None, workspace=None,
                     num_workers=0, return_lse=True, stream=None):
     """Paged split-KV decode.  Shapes: see ``include/sinkattn.h``.  Returns (out, lse)."""
@@ -134,6 +147,7 @@ def sinkattn_verify_workspace_size(q, k_pages, page_table, num_workers=0) -> int
     return int(_lib.sinkattn_verify_workspace_size(ctypes.byref(verify_dims(q, k_pages, page_table, num_workers))))
 
 
+@_on_stream
 def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=None, lse=None, workspace=None,
                     num_workers=0, return_lse=True, stream=None):
     """Attention of q_len drafted tokens per request over the paged cache (their K/V already in it).
@@ -168,6 +182,7 @@ def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
     return out, lse
 
 
+@_on_stream
 def sinkattn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, tree_mask, sinks, scale, out=None, lse=None,
                          workspace=None, num_workers=0, return_lse=True, stream=None):
     """sinkattn_verify for a draft tree: tree_mask [B, q_len] int64 on the device, bit j of mask i = drafted
@@ -225,6 +240,7 @@ def sinkattn_kv_append(k, v, cu_seqlens, start_pos, page_table, k_pages, v_pages
     _check(st, "sinkattn_kv_append")
 
 
+@_on_stream
 def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages, v_pages, num_q_heads, theta,
                           factor, original_max_position, beta_fast, beta_slow, attn_factor=0.0, interleaved=False,
                           q_out=None, stream=None):
@@ -254,6 +270,7 @@ def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages,
     return q_out
 
 
+@_on_stream
 def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_pos, sinks, scale, max_seqlen=None,
                            out=None, lse=None, return_lse=True, stream=None, share_sms=False):
     """Chunked prefill of new tokens q [T, Hq, 64] over the paged cache (their K/V already appended):
@@ -282,6 +299,7 @@ def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_po
     return out, lse
 
 
+@_on_stream
 def sinkattn_prefill(q, k, v, cu_seqlens, sinks, scale, causal=True, max_seqlen=None, out=None, lse=None,
                      return_lse=True, stream=None, share_sms=False):
     """Packed varlen prefill.  ``max_seqlen`` (an upper bound of the lengths) is required.  ``share_sms``
@@ -308,6 +326,7 @@ def sinkattn_prefill(q, k, v, cu_seqlens, sinks, scale, causal=True, max_seqlen=
     return out, lse
 
 
+@_on_stream
 def sinkattn_merge(partial_o, partial_lse, sinks=None, out=None, lse=None, return_lse=True, stream=None):
     """LSE merge of partials [S,R,H,64] / [S,R,H]; ``sinks`` adds the sink once."""
     _need(partial_o, "partial_o", torch.float32, 4)
@@ -363,18 +382,6 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
 
 _Tensor, _f32, _bf16, _i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
 _LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
-
-
-def _on_stream(fn):
-    """Runs a call with its ``stream`` argument current, so that what it allocates (outputs, workspace) belongs to the
-    stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
 
 
 def _here(t, device):
