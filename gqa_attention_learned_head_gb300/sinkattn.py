@@ -62,16 +62,13 @@ def _raw_stream(device):
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _on_stream(fn):
-    """Runs a call with its ``stream`` argument current, so that what it allocates (outputs, workspace) belongs to the
+def _empty(shape, device, dtype, stream):
+    """An output or workspace of a call on ``stream`` (None: the current one), of that stream's memory: freed, it goes back to the
     stream that uses it."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+    if stream is None:
+        return torch.empty(shape, device=device, dtype=dtype)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, device=device, dtype=dtype)
 
 
 def _need(t, name, dtype, ndim):
@@ -106,7 +103,6 @@ def sinkattn_decode_workspace_size(q, k_pages, page_table, num_workers=0) -> int
     return int(_lib.sinkattn_decode_workspace_size(ctypes.byref(decode_dims(q, k_pages, page_table, num_workers))))
 
 
-@_on_stream
 def sinkattn_decode(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=None, lse=None, workspace=None,
                     num_workers=0, return_lse=True, stream=None):
     """Paged split-KV decode.  Shapes: see ``include/sinkattn.h``.  Returns (out, lse)."""
@@ -122,14 +118,14 @@ def sinkattn_decode(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
         raise ValueError("inconsistent decode shapes")
     dims = decode_dims(q, k_pages, page_table, num_workers)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.device, q.dtype, stream)
     if lse is None and return_lse:
-        lse = torch.empty(B, Hq, device=q.device, dtype=torch.float32)
+        lse = _empty((B, Hq), q.device, torch.float32, stream)
     if workspace is None:
         nbytes = int(_lib.sinkattn_decode_workspace_size(ctypes.byref(dims)))
         if nbytes == 0:
             raise SinkAttnError(ERR_INVALID_ARG, "sinkattn_decode_workspace_size")
-        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+        workspace = _empty(nbytes, q.device, torch.uint8, stream)
     st = _lib.sinkattn_decode(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(sinks),
                               float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _stream(stream))
@@ -147,7 +143,6 @@ def sinkattn_verify_workspace_size(q, k_pages, page_table, num_workers=0) -> int
     return int(_lib.sinkattn_verify_workspace_size(ctypes.byref(verify_dims(q, k_pages, page_table, num_workers))))
 
 
-@_on_stream
 def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=None, lse=None, workspace=None,
                     num_workers=0, return_lse=True, stream=None):
     """Attention of q_len drafted tokens per request over the paged cache (their K/V already in it).
@@ -167,14 +162,14 @@ def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
         raise ValueError("inconsistent verify shapes")
     dims = verify_dims(q, k_pages, page_table, num_workers)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.device, q.dtype, stream)
     if lse is None and return_lse:
-        lse = torch.empty(B, QL, Hq, device=q.device, dtype=torch.float32)
+        lse = _empty((B, QL, Hq), q.device, torch.float32, stream)
     if workspace is None:
         nbytes = int(_lib.sinkattn_verify_workspace_size(ctypes.byref(dims)))
         if nbytes == 0:
             raise SinkAttnError(ERR_INVALID_ARG, "sinkattn_verify_workspace_size")
-        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+        workspace = _empty(nbytes, q.device, torch.uint8, stream)
     st = _lib.sinkattn_verify(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(sinks),
                               float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _stream(stream))
@@ -182,7 +177,6 @@ def sinkattn_verify(q, k_pages, v_pages, page_table, kv_lens, sinks, scale, out=
     return out, lse
 
 
-@_on_stream
 def sinkattn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, tree_mask, sinks, scale, out=None, lse=None,
                          workspace=None, num_workers=0, return_lse=True, stream=None):
     """sinkattn_verify for a draft tree: tree_mask [B, q_len] int64 on the device, bit j of mask i = drafted
@@ -201,14 +195,14 @@ def sinkattn_verify_tree(q, k_pages, v_pages, page_table, kv_lens, tree_mask, si
     Hq = q.shape[2]
     dims = verify_dims(q, k_pages, page_table, num_workers)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.device, q.dtype, stream)
     if lse is None and return_lse:
-        lse = torch.empty(B, QL, Hq, device=q.device, dtype=torch.float32)
+        lse = _empty((B, QL, Hq), q.device, torch.float32, stream)
     if workspace is None:
         nbytes = int(_lib.sinkattn_verify_workspace_size(ctypes.byref(dims)))
         if nbytes == 0:
             raise SinkAttnError(ERR_INVALID_ARG, "sinkattn_verify_workspace_size")
-        workspace = torch.empty(nbytes, device=q.device, dtype=torch.uint8)
+        workspace = _empty(nbytes, q.device, torch.uint8, stream)
     st = _lib.sinkattn_verify_tree(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens),
                                    _ptr(tree_mask), _ptr(sinks), float(scale), _ptr(out), _ptr(lse), ctypes.byref(dims),
                                    _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
@@ -240,7 +234,6 @@ def sinkattn_kv_append(k, v, cu_seqlens, start_pos, page_table, k_pages, v_pages
     _check(st, "sinkattn_kv_append")
 
 
-@_on_stream
 def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages, v_pages, num_q_heads, theta,
                           factor, original_max_position, beta_fast, beta_slow, attn_factor=0.0, interleaved=False,
                           q_out=None, stream=None):
@@ -260,7 +253,7 @@ def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages,
     if qkv.shape[1] != (num_q_heads + 2 * Hkv) * 64 or (bias is not None and bias.shape[0] != qkv.shape[1]):
         raise ValueError("qkv must be [T, (Hq + 2 Hkv) * 64] and bias [(Hq + 2 Hkv) * 64]")
     if q_out is None:
-        q_out = torch.empty(T, num_q_heads, 64, device=qkv.device, dtype=torch.bfloat16)
+        q_out = _empty((T, num_q_heads, 64), qkv.device, torch.bfloat16, stream)
     dims = paged_dims(k_pages, page_table, cu_seqlens, T, 0, num_q_heads)
     rope = RopeParams(theta, factor, original_max_position, beta_fast, beta_slow, attn_factor, int(bool(interleaved)))
     st = _lib.sinkattn_qkv_prologue(_ptr(qkv), _ptr(bias), _ptr(cu_seqlens), _ptr(start_pos), _ptr(page_table),
@@ -270,7 +263,6 @@ def sinkattn_qkv_prologue(qkv, bias, cu_seqlens, start_pos, page_table, k_pages,
     return q_out
 
 
-@_on_stream
 def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_pos, sinks, scale, max_seqlen=None,
                            out=None, lse=None, return_lse=True, stream=None, share_sms=False):
     """Chunked prefill of new tokens q [T, Hq, 64] over the paged cache (their K/V already appended):
@@ -289,9 +281,9 @@ def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_po
     _pools_match(k_pages, v_pages, D)
     dims = paged_dims(k_pages, page_table, cu_seqlens, T, max_seqlen, Hq, share_sms)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.device, q.dtype, stream)
     if lse is None and return_lse:
-        lse = torch.empty(T, Hq, device=q.device, dtype=torch.float32)
+        lse = _empty((T, Hq), q.device, torch.float32, stream)
     st = _lib.sinkattn_prefill_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(cu_seqlens),
                                      _ptr(start_pos), _ptr(sinks), float(scale), _ptr(out), _ptr(lse),
                                      ctypes.byref(dims), _stream(stream))
@@ -299,7 +291,6 @@ def sinkattn_prefill_paged(q, k_pages, v_pages, page_table, cu_seqlens, start_po
     return out, lse
 
 
-@_on_stream
 def sinkattn_prefill(q, k, v, cu_seqlens, sinks, scale, causal=True, max_seqlen=None, out=None, lse=None,
                      return_lse=True, stream=None, share_sms=False):
     """Packed varlen prefill.  ``max_seqlen`` (an upper bound of the lengths) is required.  ``share_sms``
@@ -317,16 +308,15 @@ def sinkattn_prefill(q, k, v, cu_seqlens, sinks, scale, causal=True, max_seqlen=
         raise ValueError("inconsistent prefill shapes")
     dims = PrefillDims(cu_seqlens.shape[0] - 1, T, int(max_seqlen), Hq, k.shape[1], D, int(bool(share_sms)))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.device, q.dtype, stream)
     if lse is None and return_lse:
-        lse = torch.empty(T, Hq, device=q.device, dtype=torch.float32)
+        lse = _empty((T, Hq), q.device, torch.float32, stream)
     st = _lib.sinkattn_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(cu_seqlens), _ptr(sinks), float(scale),
                                int(bool(causal)), _ptr(out), _ptr(lse), ctypes.byref(dims), _stream(stream))
     _check(st, "sinkattn_prefill")
     return out, lse
 
 
-@_on_stream
 def sinkattn_merge(partial_o, partial_lse, sinks=None, out=None, lse=None, return_lse=True, stream=None):
     """LSE merge of partials [S,R,H,64] / [S,R,H]; ``sinks`` adds the sink once."""
     _need(partial_o, "partial_o", torch.float32, 4)
@@ -338,9 +328,9 @@ def sinkattn_merge(partial_o, partial_lse, sinks=None, out=None, lse=None, retur
         raise ValueError("partial_lse must be [S, R, H]")
     dims = MergeDims(S, R, H, D)
     if out is None:
-        out = torch.empty(R, H, D, device=partial_o.device, dtype=torch.bfloat16)
+        out = _empty((R, H, D), partial_o.device, torch.bfloat16, stream)
     if lse is None and return_lse:
-        lse = torch.empty(R, H, device=partial_o.device, dtype=torch.float32)
+        lse = _empty((R, H), partial_o.device, torch.float32, stream)
     st = _lib.sinkattn_merge(_ptr(partial_o), _ptr(partial_lse), _ptr(sinks), _ptr(out), _ptr(lse),
                              ctypes.byref(dims), _stream(stream))
     _check(st, "sinkattn_merge")
@@ -382,6 +372,18 @@ def sinkattn_decode_noalloc(q, k_pages, v_pages, page_table, kv_lens, sinks, sca
 
 _Tensor, _f32, _bf16, _i32 = torch.Tensor, torch.float32, torch.bfloat16, torch.int32
 _LOGIT_DTYPES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _on_stream(fn):
+    """Runs a call with its ``stream`` argument current, so that what it allocates (outputs, workspace) belongs to the
+    stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
 
 
 def _here(t, device):
