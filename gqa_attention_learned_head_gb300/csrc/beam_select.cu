@@ -6,11 +6,13 @@
 // tokens, and only M candidates a row meet the rows of the group.
 //   Sum.  Every thread keeps sums of 2^(x L - r) (L = log2 e in 32 bits) against an integer r near its
 //   largest x L: moving to another r multiplies by a power of two, which is exact, so how a row is cut
-//   changes nothing but the order of additions.  Threads hold 32-bit sums of a few hundred terms, everything
-//   above that is in pairs of floats (48 bits): the scores of two beams may lie next to each other.
-//   lse = (r + log2 s) / L with the same rounded L, so its rounding cancels to first order.  Where the largest
-//   logit is beyond +-2^20 (rows of nothing but a type's lowest value) the share is read again and summed as
-//   e^(x - m).
+//   changes nothing but the order of additions.  Threads hold 32-bit sums of up to 1024 terms, everything above that is in
+//   pairs of floats (48 bits) and adds nothing to their error.  lse = (r + log2 s) / L with the same rounded L: what its
+//   rounding does to the exponents cancels but for 1.3e-8 of the row's entropy.  So the logarithm of the sum is off by at
+//   most 8e-6 (four sums of 256 additions a thread in a share of 262144 tokens, were all roundings to lean one way; 5e-6 up to
+//   131072; on random rows none of it shows beside the rounding of a 32-bit score), and beams whose scores are closer than that
+//   may come in either order.  Where the largest logit is beyond +-2^20 (rows of nothing but a type's lowest value) the share
+//   is read again and summed as e^(x - m), one sum a thread: 3.1e-5.
 //   Best tokens.  The row is cut into groups of 32 consecutive tokens whose maxima stay in shared memory.  The M
 //   best tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there
 //   are M tokens ahead.  So the pass over the row has no list to maintain; afterwards the M-th best of the
@@ -24,9 +26,9 @@
 //
 // Measured (GB300, calls back to back from a graph): 64 groups of 8 rows of 200000 bf16 logits 43 us, 4.8 TB/s = 70% of
 // the copy rate: the pass over the rows takes 29 us (7 TB/s), its tail (threshold, 64 x 32 tokens read again and ranked)
-// 5 us, the merge 3.5, the rest is starts.  32 groups of 8 rows of 50021 f32 logits 18.7 us (51 MB: 7.5 us of reading); one
-// group of 4 rows of 32000 7.9 us, all latency.  Five or six CTAs an SM (fewer registers, spills) and more, smaller shares
-// were slower; 64-bit sums and 128-bit keys in the merge took 19.5 us where pairs of floats take 3.5.
+// 5 us, the merge 3.5, the rest is starts; f16 the same.  32 groups of 8 rows of 50021 f32 logits 18.7 us (51 MB: 7.5 us of
+// reading), f16 14.9; one group of 4 rows of 32000 7.9 us in any type, all latency.  Five or six CTAs an SM (fewer registers,
+// spills) and more, smaller shares were slower; 64-bit sums and 128-bit keys in the merge took 19.5 us where pairs of floats take 3.5.
 #include "args_beam.h"
 #include "errors_beam.h"
 #include "ptx.cuh"

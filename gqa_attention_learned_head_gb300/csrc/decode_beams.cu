@@ -24,7 +24,7 @@
 // A row fills a quarter or half of the tile's rows where R allows it: the query rows are then loaded two or four
 // times, every copy takes its half or quarter of a tile's keys (the other keys' weights stay zero, so the products
 // keep their form) and a state of its own, and the copies' states are put together at a piece's end.  All four
-// softmax warps work then: with 8 rows of 8 heads over one long prompt the call took 186 us instead of 202.
+// softmax warps work then: 4 groups of 8 rows of 8 heads with 131072 tokens take 176 us, with one copy 201; 4 rows 168 and 180.
 // A row's own pages are weights of zero for every other row of the group: a warp whose rows see none of its keys of a
 // tile takes no maximum and no exponential of them.
 // A weight of zero times a NaN or an infinity in such a page is a NaN in rows that do not hold it: rows whose sums come
@@ -36,10 +36,11 @@
 // 57 for 32 groups of 8 rows).  Every wait is bounded.
 //
 // Measured (GB300, 64 query and 8 KV heads, calls back to back from a graph): 4 groups of 8 rows with 131072 tokens
-// 175 us, 6.25 TB/s = 92% of the copy rate (HBM; row by row the pages are 8.6 GB, 1.27 ms).  32 groups of 8 rows with
-// 512 to 4096 tokens, 128 of them a row's own, 53.9 us against 30.1 of reading: the tiles stream at the copy rate (20 of
+// 176 us, 6.2 TB/s = 92% of the copy rate (HBM); sinkattn_decode on the 32 rows takes 686 us (8.6 GB of pages, many of them
+// from L2).  4 rows a group, four copies of the query rows: 168 us, 95%.  32 groups of 8 rows with 512 to 4096 tokens, 128 of them
+// a row's own, 54 us against 30.1 of reading (sinkattn_decode on the 256 rows 132 us): the tiles stream at the copy rate (20 of
 // 1.5 us a CTA), but 11 us pass before the first scores (the plan 4, its end to the shares' start 4, the first pages 3),
-// some 3 us at each piece's end, and the merge takes about 5.  More than 64 query rows: 16 rows a group 84.5 us against
+// some 3 us at each piece's end, and the merge takes about 5.  More than 64 query rows: 16 rows a group 85 us against
 // 39.3 of reading, the softmax's instructions (one thread a row and all 128 keys, two warps a scheduler).
 #include "args_beams.h"
 #include "args_merge.h"

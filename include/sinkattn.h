@@ -431,7 +431,9 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
  *     score(k, v) = scores[n][k] + logits[n][k][v] - ln sum_u exp(logits[n][k][u]),
  * in descending order; equal scores go to the lower beam, then the lower token.  Sums of exponentials are
  * held in 32 bits per thread (of at most 1024 tokens); everything above that, and the scores that are
- * compared, in pairs of floats (48 bits); out_scores are those rounded to f32.
+ * compared, in pairs of floats (48 bits); out_scores are those rounded to f32.  A row's logarithm of the sum is
+ * off by at most 8e-6 (3.1e-5 where its largest logit is beyond +-2^20), and beams whose scores lie closer than
+ * that may come in either order.
  *
  *   logits    [N, K, V]  f32, bf16 or f16; row (n, k) starts row_stride elements after row (n, k - 1)
  *   scores    [N, K]     f32   running log-probability of each beam; -inf: the beam is not in use, its
@@ -589,7 +591,9 @@ size_t sinkattn_decode_beams_workspace_size(const sinkattn_beams_dims_t *dims);
  *   out        [N, K, Hq, 64]          bf16
  *   lse        [N, K, Hq]              f32 natural log, or NULL
  *   workspace  at least sinkattn_decode_beams_workspace_size(dims) bytes, 256-byte aligned; it needs no
- *              initialisation and must not be shared by calls that may overlap.
+ *              initialisation and must not be shared by calls that may overlap.  Most of it is 16 bytes for
+ *              every entry of page_table (a list of distinct pages has room for all of them), whatever
+ *              the rows hold: 256 groups of 8 rows of 8192 columns need 268 MB.
  *
  * Errors and the handling of bad page ids and lengths are those of sinkattn_decode.
  */
