@@ -92,8 +92,8 @@ KERNEL_SOURCES = {
                           "args_common.h"],
     "prefill_tc_kernel": ["prefill_tc.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
                           "args_common.h"],
-    "prefill_pp_kernel_paged": ["prefill_pp.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh", "args_prefill.h",
-                                "args_common.h"],
+    "prefill_pp_kernel_paged": ["prefill_pp.cu", "ptx.cuh", "smem_limit.h", "tc_tile.cuh", "tile_order.cuh",
+                                "args_prefill.h", "args_common.h"],
     "qkv_prologue_kernel": ["prologue.cu", "ptx.cuh", "args_paged.h", "args_common.h"],
 }
 

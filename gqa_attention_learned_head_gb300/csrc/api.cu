@@ -92,15 +92,18 @@ bool encode_cached(CUtensorMap* map, int rank, const void* base, const cuuint64_
             *map = cache[i].map;
             return true;
         }
-    // the encoder is a driver call and needs a context, which a host thread whose first use of the GPU this is does not have
-    // yet: a query of a kernel makes the device's own current, or leaves the thread's as it is
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, take_error_kernel) != cudaSuccess) return false;
     const cuuint32_t estride[3] = {1, 1, 1};
-    if (g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
-                 estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-        return false;
+    auto encode = [&]() {
+        return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box,
+                        estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    if (!encode()) {
+        // the encoder is a driver call and needs a context, which a host thread whose first use of the GPU this is does not
+        // have yet: a query of a kernel makes the device's own current, or leaves the thread's as it is
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, take_error_kernel) != cudaSuccess || !encode()) return false;
+    }
     Entry& e = cache[next];
     e.base = base;
     e.rank = rank;

@@ -10,8 +10,8 @@
 //   pairs of floats (48 bits) and adds nothing to their error.  lse = (r + log2 s) / L with the same rounded L: what its
 //   rounding does to the exponents cancels but for 1.3e-8 of the row's entropy.  So the logarithm of the sum is off by at
 //   most 8e-6 (four sums of 256 additions a thread in a share of 262144 tokens, were all roundings to lean one way; 5e-6 up to
-//   131072; on random rows none of it shows beside the rounding of a 32-bit score), and beams whose scores are closer than that
-//   may come in either order.  Where the largest logit is beyond +-2^20 (rows of nothing but a type's lowest value) the share
+//   131072; on random rows none of it shows beside the rounding of a 32-bit score), and beams whose scores are closer than
+//   twice that may come in either order.  Where the largest logit is beyond +-2^20 (rows of nothing but a type's lowest value) the share
 //   is read again and summed as e^(x - m), one sum a thread: 3.1e-5.
 //   Best tokens.  The row is cut into groups of 32 consecutive tokens whose maxima stay in shared memory.  The M
 //   best tokens lie in the M best groups (ordered by maximum, then position): of any other group's token there

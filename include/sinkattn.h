@@ -433,7 +433,7 @@ size_t sinkattn_beam_select_workspace_size(const sinkattn_beam_dims_t *dims);
  * held in 32 bits per thread (of at most 1024 tokens); everything above that, and the scores that are
  * compared, in pairs of floats (48 bits); out_scores are those rounded to f32.  A row's logarithm of the sum is
  * off by at most 8e-6 (3.1e-5 where its largest logit is beyond +-2^20), and beams whose scores lie closer than
- * that may come in either order.
+ * twice that may come in either order.
  *
  *   logits    [N, K, V]  f32, bf16 or f16; row (n, k) starts row_stride elements after row (n, k - 1)
  *   scores    [N, K]     f32   running log-probability of each beam; -inf: the beam is not in use, its
