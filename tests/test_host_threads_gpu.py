@@ -148,3 +148,50 @@ def test_a_small_batch_leaves_a_large_ones_limits(S, make, Hq):
         for x, y in zip(other, b.submit(run, small).result()):
             assert torch.equal(x, y)
     assert S.sinkattn_get_error() == 0
+
+
+def test_beam_steps_at_once(S):
+    """Threads with a stream each, all in selections, forks, copies and decodes of their own at the same time: the same bits as
+    alone."""
+    def state(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        N, K, V, mp = 3 + seed, 4, 5001 + 700 * seed, 20
+        P = N * K * mp + 50
+        table = torch.randperm(N * K * mp, generator=g, device="cuda").to(torch.int32).view(N, K, mp)
+        table[:, 1:, :12] = table[:, :1, :12]
+        lens = torch.randint(mp * 16 - 30, mp * 16 - 1, (N, 1), generator=g, device="cuda", dtype=torch.int32).expand(N, K).contiguous()
+        refs = torch.bincount(table.view(-1).long(), minlength=P).to(torch.int32)
+        pool = [torch.randn(P, 2, 16, 64, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2)]
+        q = torch.randn(N, K, 16, 64, generator=g, device="cuda").to(torch.bfloat16)
+        return (torch.randn(N, K, V, generator=g, device="cuda"), -torch.rand(N, K, generator=g, device="cuda"),
+                table.view(N * K, mp), lens.view(-1), refs, pool, q, torch.randn(16, generator=g, device="cuda"))
+
+    def step(s, stream):
+        z, c, table, lens, refs, pool, q, sinks = s
+        N, K = c.shape
+        with torch.cuda.stream(stream):
+            k, v = pool[0].clone(), pool[1].clone()
+            scores, parents, tokens = S.sinkattn_beam_select(z, c, K)
+            new, room, counts, copies = S.sinkattn_pages_fork(table, lens, parents.view(-1), refs, grow=1)
+            S.sinkattn_kv_copy(k, v, copies)
+            out, lse = S.sinkattn_decode_beams(q, k, v, new.view(N, K, -1), (room - 1).view(N, K), sinks, 0.125)
+        return scores, parents, tokens, new, room, counts, copies, out, lse
+
+    states = [state(i) for i in range(4)]
+    main = torch.cuda.current_stream()
+    alone = [[t.clone() for t in step(s, main)] for s in states]
+    torch.cuda.synchronize()
+    assert S.sinkattn_get_error() == 0
+
+    def run(i):
+        stream = torch.cuda.Stream()
+        got = [step(states[i], stream) for _ in range(40)]
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as pool:
+        results = [f.result() for f in [pool.submit(run, i) for i in range(4)]]
+    for got, want in zip(results, alone):
+        for outs in got:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert S.sinkattn_get_error() == 0
