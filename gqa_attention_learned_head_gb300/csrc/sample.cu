@@ -34,6 +34,7 @@
 #include "args_sample.h"
 #include "errors_beam.h"
 #include "ptx.cuh"
+#include "sample_sums.h"
 #include "smem_limit.h"
 
 namespace sinkattn {
@@ -169,27 +170,7 @@ __device__ __forceinline__ float bound_of(uint32_t k) {
     return z == 0.f && (__float_as_uint(z) >> 31) ? __uint_as_float(0x80000001u) : z;
 }
 
-// ---------------------------------------------------------------- sums in two floats
-// A sum as h + l, |l| at most half a step of h: about 46 bits.  (64-bit arithmetic runs at 1/64 of the 32-bit rate on this GPU; this
-// takes some ten 32-bit instructions.)
-struct Pair {
-    float h, l;
-};
-__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
-    const float s = a.h + b.h, t = s - a.h;
-    const float e = ((a.h - (s - t)) + (b.h - t)) + (a.l + b.l);
-    const float h = s + e;
-    return {h, e - (h - s)};
-}
-__device__ __forceinline__ Pair times(Pair a, float x) {
-    const float p = __fmul_rn(a.h, x), e = __fmaf_rn(a.h, x, -p) + a.l * x;
-    const float h = p + e;
-    return {h, e - (h - p)};
-}
-__device__ __forceinline__ Pair times(Pair a, unsigned n) {  // (both parts of n are exact in f32)
-    return times(a, (float)(n & ~0xFFFu)) + times(a, (float)(n & 0xFFFu));
-}
-__device__ __forceinline__ bool operator<(Pair a, Pair b) { return a.h < b.h || (a.h == b.h && a.l < b.l); }
+// ---------------------------------------------------------------- sums in two floats, within a warp
 __device__ __forceinline__ double value(Pair a) { return (double)a.h + (double)a.l; }
 __device__ __forceinline__ Pair shfl_up(Pair a, int o) {
     return {__shfl_up_sync(0xffffffffu, a.h, o), __shfl_up_sync(0xffffffffu, a.l, o)};
@@ -573,6 +554,17 @@ struct Row {
         next = sm->found_next;
         __syncthreads();
     }
+    // The least of the block's numbers, in every thread.
+    __device__ int lowest(int x) {
+        if (tid == 0) sm->found = x;
+        x = __reduce_min_sync(0xffffffffu, x);
+        __syncthreads();
+        if (lane == 0) atomicMin(&sm->found, x);
+        __syncthreads();
+        x = sm->found;
+        __syncthreads();
+        return x;
+    }
     // The bin of sm->tot that holds the k-th token (k >= 1): its number, -1 if there are fewer, and the tokens before it.
     __device__ int bin_of_rank(unsigned k, unsigned& above) {
         constexpr int kEach = kBins / kThreads;
@@ -759,16 +751,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
             est += w[i];
         }
         float b = r.before(est, sm->scan_f, all);
-        if (r.tid == 0) sm->found = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-            if (b < p * all && b + w[i] >= p * all) sm->found = r.tid * kEach + i;
-            b += w[i];
-        }
-        __syncthreads();
-        pbin = sm->found;
-        __syncthreads();
+        pbin = min(r.lowest(first_reaching(b, w, n, p * all, r.tid * kEach, kBins)), kBins - 1);
         r.neighbours(pbin, pbin_prev, pbin_next);
     }
 
@@ -914,20 +897,17 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
                 mass = mass + w[i];
             }
             Pair b = above + r.before(mass, sm->scan_p, total);
-            if (r.tid == 0) sm->found = -1;
-            __syncthreads();
+            const int mine = first_reaching(b, w, n, target, r.tid * kEach, kBins);
+            int bin = r.lowest(mine);
+            if (bin == kBins) {
+                bin = -1;
+            } else if (bin == mine) {  // (one thread's: bins are dealt apart)
+                sm->found_mass = make_float2(b.h, b.l);
 #pragma unroll
-            for (int i = 0; i < kEach; ++i) {
-                const Pair next = b + w[i];
-                if (b < target && !(next < target) && n[i]) {
-                    sm->found = r.tid * kEach + i;
-                    sm->found_mass = make_float2(b.h, b.l);
-                    sm->found_count = n[i];
-                }
-                b = next;
+                for (int i = 0; i < kEach; ++i)
+                    if (bin == r.tid * kEach + i) sm->found_count = n[i];
             }
             __syncthreads();
-            const int bin = sm->found;
             const Pair b0 = {sm->found_mass.x, sm->found_mass.y};
             const unsigned here = sm->found_count;
             __syncthreads();
