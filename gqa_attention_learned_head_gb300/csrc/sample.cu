@@ -15,10 +15,10 @@
 //    weights above that are summed token by token, and those sums, with the sorted tokens or the counts of single values below,
 //    decide.  A wrong guess is seen in the sums and corrected, never used.
 //  * A token is picked by comparing sums over as many as 10^5 tokens whose weights are 10^-6 of the total each: sums in 32 bits (6e-8)
-//    would pick another than exact arithmetic in a few rows of a thousand.  Sums are held in two floats (46 bits) and weights to 2^-30,
-//    with errors that differ from token to token and mostly cancel: as y = (z - m) log2(e) / t, 2^y = 2^n 2^(i/32) 2^r, the middle
-//    factor in two floats from a table held by a warp's lanes, the last a polynomial.  (64-bit arithmetic runs at 1/64 of the
-//    32-bit rate here.  Weights carried to 2^-38 cost 1.6 times as much: 127 us for the largest case below.)
+//    would pick another than exact arithmetic in a few rows of a thousand.  Sums are held in two floats (46 bits) and weights to
+//    2^-28.5 (sample_weights.h): 2^y = 2^n 2^(i/32) 2^r, the middle factor in two floats from a table held by a warp's lanes, the last a
+//    polynomial.  Errors of different logits mostly cancel, those of equal ones do not.  (64-bit arithmetic runs at 1/64 of the 32-bit
+//    rate here.  Weights carried to 2^-38 cost 1.6 times as much: 127 us for the largest case below.)
 //  * Sums are kept by warp; each warp owns a run of the row in index order, so the token's place is found among at most 64 runs, then
 //    in one of them.  Kept ties need no list: the kept weights up to a token are (those with z > z*) + w(z*) min(r, number of
 //    z = z* so far).
@@ -26,7 +26,7 @@
 // Bound by instructions, not by HBM, which the row's one reading leaves idle 95% of the time.  Measured (GB300): 256 rows of 50021
 // f32, settings of their own, 96 us (7.6 of reading): a CTA takes 27 us (load 2.3, maximum 2, first bins 5, list and sort 8 to
 // 12, sums 2.5, the rest waits of eight exchanges within the cluster), 1024 CTAs in three waves; 64 rows of 200000 bf16, top-p of a flat
-// distribution, 90 us (3.8): weights of every token twice the 30000 clocks that one sum over a CTA's 25000 tokens takes,
+// distribution, 93 us (3.8): weights of every token twice the 30000 clocks that one sum over a CTA's 25000 tokens takes,
 // with three CTAs on an SM.  One row of 32000: 15 us, latency.  Three CTAs an SM (80 registers) instead of two: 10% faster.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +35,7 @@
 #include "errors_beam.h"
 #include "ptx.cuh"
 #include "sample_sums.h"
+#include "sample_weights.h"
 #include "smem_limit.h"
 
 namespace sinkattn {
@@ -196,60 +197,41 @@ __device__ __forceinline__ V lanes_below(V x, int lane) {
 }
 
 // ---------------------------------------------------------------- weights
-// 2^(i / 32) in two floats, from the definition to 60 digits.
-__device__ const float2 kRoots[32] = {
-    {1.e+00f, 0.e+00f}, {1.0218972e+00f, -4.81156e-08f}, {1.0442737e+00f, 4.83347e-08f}, {1.0671405e+00f, -5.933752e-08f},
-    {1.0905077e+00f, -1.307754e-08f}, {1.1143868e+00f, -5.43554e-08f}, {1.1387886e+00f, 5.3862223e-08f}, {1.1637249e+00f, -4.0514415e-08f},
-    {1.1892071e+00f, 3.7976353e-08f}, {1.2152474e+00f, -3.267395e-08f}, {1.2418578e+00f, 4.496838e-08f}, {1.269051e+00f, 1.4193333e-09f},
-    {1.2968396e+00f, -4.0189995e-08f}, {1.3252367e+00f, -3.4963733e-08f}, {1.3542556e+00f, -1.0123349e-08f}, {1.38391e+00f, -5.8755774e-08f},
-    {1.4142135e+00f, 2.4203235e-08f}, {1.4451808e+00f, 3.3242e-08f}, {1.4768262e+00f, -4.500899e-08f}, {1.5091645e+00f, -2.4959373e-08f},
-    {1.5422108e+00f, 8.070905e-09f}, {1.5759809e+00f, -5.6610254e-08f}, {1.6104903e+00f, 9.836217e-09f}, {1.6457555e+00f, -5.124972e-08f},
-    {1.6817929e+00f, -2.4755327e-08f}, {1.7186193e+00f, -4.8496176e-08f}, {1.7562522e+00f, -9.23577e-09f}, {1.7947091e+00f, -1.1415045e-08f},
-    {1.8340081e+00f, -1.1239278e-08f}, {1.8741677e+00f, -4.6630056e-08f}, {1.9152066e+00f, 9.845328e-09f}, {1.9571441e+00f, -1.7021804e-08f}};
+__device__ const float2 kRoots[32] = SINKATTN_ROOTS;
 
-struct Weight {
-    float m, ch, cl;  // largest logit; log2(e) / t in two floats
-    float th, tl;     // this lane's entry of the table: 2^(lane / 32) in two floats
+// Two numbers at a time.
+struct TwoByTwo {
+    using F = float2;
+    static __device__ __forceinline__ F all(float x) { return make_float2(x, x); }
+    static __device__ __forceinline__ F add(F a, F b) { return fadd2(a, b); }
+    static __device__ __forceinline__ F mul(F a, F b) { return fmul2(a, b); }
+    static __device__ __forceinline__ F fma(F a, F b, F c) { return ffma2(a, b, c); }
 };
 
-// Weights of two logits, each as hi + lo with lo at most 2^-6 of hi; every lane of the warp calls.  With y = (z - m) log2(e) / t,
-// k = rint(32 y) and r = y - k / 32, 2^y = 2^(k / 32) (1 + r c1 + r^2 c2 + ..), |r| at most 1/64: hi is the table's entry, lo all that
-// follows, in one float: off by at most 2^-30 of the weight, differently for each token.  kExact: z - m may have to be rounded
-// (32-bit logits); of 16-bit ones only the few next to zero are, by 2^-25.
-template <bool kExact>
+struct Weight : RowScale {
+    float th, tl;  // this lane's entry of the table: 2^(lane / 32) in two floats
+};
+
+// Weights of two logits, each as hi + lo with lo at most half a step of hi; every lane of the warp calls.
 __device__ __forceinline__ float2 weights2(const Weight& g, float2 z, float2& lo) {
-    constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
-    float2 dl, d;
-    if (kExact) d = two_sum(z, both(-g.m), dl);
-    else d = fadd2(z, both(-g.m));
-    const float2 y = fmul2(d, both(g.ch));
-    const float2 t = ffma2(y, both(32.f), both(kMagic));
-    const float2 k = fmul2(fadd2(t, both(-kMagic)), both(-1.f / 32.f));
-    float2 r = ffma2(d, both(g.cl), ffma2(d, both(g.ch), k));
-    if (kExact) r = ffma2(dl, both(g.ch), r);
-    const int k0 = __float_as_int(t.x) - 0x4B400000, k1 = __float_as_int(t.y) - 0x4B400000;
+    float2 y, k, r, h, l;
+    split_power<TwoByTwo>(g, z, y, k, r);
+    const int k0 = __float_as_int(k.x) - 0x4B400000, k1 = __float_as_int(k.y) - 0x4B400000;
     const float2 th = make_float2(__shfl_sync(0xffffffffu, g.th, k0 & 31), __shfl_sync(0xffffffffu, g.th, k1 & 31));
     const float2 tl = make_float2(__shfl_sync(0xffffffffu, g.tl, k0 & 31), __shfl_sync(0xffffffffu, g.tl, k1 & 31));
-    // 2^r - 1 = r (ln 2 + r (ln 2^2 / 2 + r (ln 2^3 / 6 + r (ln 2^4 / 24 + r ln 2^5 / 120))))
-    float2 q = ffma2(r, both(0.00133335581f), both(0.00961812911f));
-    q = ffma2(r, q, both(0.0555041087f));
-    q = ffma2(r, q, both(0.240226507f));
-    q = ffma2(r, q, both(0.693147181f));
-    q = fmul2(r, q);
-    const float2 v = ffma2(th, q, tl);
-    // times 2^n; below 2^-110 a weight is nothing
-    const bool in0 = y.x > -110.f, in1 = y.y > -110.f;
-    const float2 s = make_float2(in0 ? __int_as_float(((k0 >> 5) + 127) << 23) : 0.f, in1 ? __int_as_float(((k1 >> 5) + 127) << 23) : 0.f);
-    lo = make_float2(in0 ? v.x * s.x : 0.f, in1 ? v.y * s.y : 0.f);
-    return make_float2(in0 ? th.x * s.x : 0.f, in1 ? th.y * s.y : 0.f);
+    root_times_power<TwoByTwo>(th, tl, r, h, l);
+    // times 2^n
+    const bool in0 = y.x > g.least, in1 = y.y > g.least;
+    const int bias = 127 - g.base;
+    const float2 s = make_float2(in0 ? __int_as_float(((k0 >> 5) + bias) << 23) : 0.f, in1 ? __int_as_float(((k1 >> 5) + bias) << 23) : 0.f);
+    lo = make_float2(in0 ? l.x * s.x : 0.f, in1 ? l.y * s.y : 0.f);
+    return make_float2(in0 ? h.x * s.x : 0.f, in1 ? h.y * s.y : 0.f);
 }
 // The weight of one logit a lane; all lanes call.
-template <bool kExact>
 __device__ __forceinline__ Pair weight1(const Weight& g, float z) {
     float2 lo;
-    const float2 hi = weights2<kExact>(g, make_float2(z, z), lo);
-    const float h = hi.x + lo.x;
-    return {h, lo.x - (h - hi.x)};
+    const float2 hi = weights2(g, make_float2(z, z), lo);
+    return {hi.x, lo.x};
 }
 
 // A first bin: falls with the logit, monotone because both roundings are, and 0 for the largest whatever its size (c32:
@@ -395,7 +377,7 @@ struct Row {
 #pragma unroll
         for (int i = 0; i < kPer; i += 2) {
             float2 vl, e;
-            const float2 v = weights2<kDrop == 0>(g, make_float2(z[i], z[i + 1]), vl);
+            const float2 v = weights2(g, make_float2(z[i], z[i + 1]), vl);
             const bool t0 = take(z[i]), t1 = take(z[i + 1]);
             hi = two_sum(hi, make_float2(t0 ? v.x : 0.f, t1 ? v.y : 0.f), e);
             lo = fadd2(lo, fadd2(e, make_float2(t0 ? vl.x : 0.f, t1 ? vl.y : 0.f)));
@@ -447,7 +429,7 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < kPer; i += 2) {
                 float2 vl, e;
-                const float2 v = weights2<kDrop == 0>(g, make_float2(z[i], z[i + 1]), vl);
+                const float2 v = weights2(g, make_float2(z[i], z[i + 1]), vl);
                 const bool a0 = z[i] > zat, a1 = z[i + 1] > zat, r0 = !a0 && z[i] > zlo, r1 = !a1 && z[i + 1] > zlo;
                 hi = two_sum(hi, make_float2(a0 ? v.x : 0.f, a1 ? v.y : 0.f), e);
                 lo = fadd2(lo, fadd2(e, make_float2(a0 ? vl.x : 0.f, a1 ? vl.y : 0.f)));
@@ -712,13 +694,8 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
     }
 
     Weight g;
-    g.m = m;
+    static_cast<RowScale&>(g) = row_scale(m, t);
     {
-        constexpr float kLog2eH = 1.442695f, kLog2eL = 1.925963033500927e-08f;  // (their sum is log2(e) to 2^-49)
-        g.ch = __fdiv_rn(kLog2eH, t);
-        g.cl = __fdiv_rn(__fmaf_rn(-g.ch, t, kLog2eH) + kLog2eL, t);
-        if (!(g.ch < 3e38f)) g.ch = 3e38f, g.cl = 0.f;      // a temperature so small that only the largest logits count
-        if (!(t < -kNegInf)) g.ch = g.cl = 0.f;             // one so large that all count alike
         const float2 root = kRoots[r.lane];
         g.th = root.x;
         g.tl = root.y;
@@ -766,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
                 const int j = r.tid * kEach + i;
-                w[i] = weight1<kDrop == 0>(g, of_key<kDrop>(j < stay ? sm->hist[j] : top));
+                w[i] = weight1(g, of_key<kDrop>(j < stay ? sm->hist[j] : top));
                 if (j >= stay) w[i] = {0.f, 0.f};
                 mass = mass + w[i];
             }
@@ -855,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
             const Pair above = r.shared_sum(s, 0);
             if (!known) {
                 Pair all = above + r.shared_sum(s, 2);
-                if (bottom_ties) all = all + times(weight1<kDrop == 0>(g, of_key<kDrop>(bottom)), bottom_ties);
+                if (bottom_ties) all = all + times(weight1(g, of_key<kDrop>(bottom)), bottom_ties);
                 target = times(all, p);
                 known = true;
             }
@@ -893,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
                 const uint32_t lo = max(klo, hi - min(hi, (1u << shift) - 1u));
                 n[i] = sm->tot[bin];
                 if (bottom_ties && shift == 0 && hi == bottom) n[i] = min(n[i], bottom_ties);
-                w[i] = times(weight1<kDrop == 0>(g, of_key<kDrop>(lo + (hi - lo) / 2)), n[i]);
+                w[i] = times(weight1(g, of_key<kDrop>(lo + (hi - lo) / 2)), n[i]);
                 mass = mass + w[i];
             }
             Pair b = above + r.before(mass, sm->scan_p, total);
@@ -924,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
             if (shift == 0) {
                 // of the ties, those before which the sum is still below the target
                 keep = khi - (uint32_t)bin;
-                const Pair wk = weight1<kDrop == 0>(g, of_key<kDrop>(keep));
+                const Pair wk = weight1(g, of_key<kDrop>(keep));
                 if (r.tid == 0) {
                     const double want = ceil((value(target) - value(b0)) / value(wk));
                     sm->found_count = want < 1.0 ? 1u : want > (double)here ? here : (unsigned)want;
@@ -974,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
         seg_a = seg_a + r.sum(g, keep, summed, n);
         s = r.share(seg_a, Pair{0.f, 0.f}, n);
     }
-    const Pair wk = weight1<kDrop == 0>(g, of_key<kDrop>(ties ? keep : top));
+    const Pair wk = weight1(g, of_key<kDrop>(ties ? keep : top));
     // kept weight up to a place: those above `keep` before it, and as many of its ties as are kept
     auto kept = [&](Pair sum, unsigned n) { return ties ? sum + times(wk, min(n, ties)) : sum; };
     Pair at_a;  // before the place looked for
@@ -1066,7 +1043,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
 #pragma unroll
     for (int i = 0; i < kPer; i += 2) {
         float2 vl;
-        const float2 v = weights2<kDrop == 0>(g, make_float2(z[i], z[i + 1]), vl);
+        const float2 v = weights2(g, make_float2(z[i], z[i + 1]), vl);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const bool takes = key[i + j] > keep || (key[i + j] == keep && ct < ties);
@@ -1074,13 +1051,13 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
                 token = (int)first + (list ? sm->list_at[ow][(best * 32 + r.lane) * kPer + i + j] : r.token(a0 + best * 32 + r.lane, i + j));
                 picked = z[i + j];
             }
-            if (key[i + j] > keep) ca = ca + (j ? Pair{v.y, vl.y} : Pair{v.x, vl.x});  // (as far apart as they are, the sum joins them)
+            if (key[i + j] > keep) ca = ca + (j ? Pair{v.y, vl.y} : Pair{v.x, vl.x});
             ct += key[i + j] == keep;
         }
     }
     if (r.lane == who) {
         a.out_tokens[row] = token;
-        if (a.out_logprobs) a.out_logprobs[row] = (float)(((double)picked - (double)m) / (double)t - log(value(Z)));
+        if (a.out_logprobs) a.out_logprobs[row] = (float)(((double)picked - (double)m) / (double)t - (log(value(Z)) + short_of(g, m, t)));
     }
 }
 
