@@ -952,6 +952,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
         s = r.share(seg_a, Pair{0.f, 0.f}, n);
     }
     const Pair wk = weight1(g, of_key<kDrop>(ties ? keep : top));
+    if (!(wk.h > 0.f)) ties = 0;  // (what has no weight is not picked)
     // kept weight up to a place: those above `keep` before it, and as many of its ties as are kept
     auto kept = [&](Pair sum, unsigned n) { return ties ? sum + times(wk, min(n, ties)) : sum; };
     Pair at_a;  // before the place looked for
@@ -976,7 +977,9 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
     }
     if (owner / kWarps != (int)r.rank) return;
 
-    // ---- the step of that run, every warp of its CTA summing some
+    // ---- the last step of that run that has some kept weight and begins at or before the target, every warp of its CTA summing some
+    // (Whether a step, a lane or a token has weight is asked of its own sum and count, not of the sums before and behind it: these may
+    // round to the same, and a run be found whose steps all do.  The first that has weight begins where the run does, so there is one.)
     const int ow = owner % kWarps;
     const int a0 = min(words, ow * run), a1 = min(words, a0 + run);
     const bool list = r.listed(ties ? keep : keep + 1u, 0xFFFFFFFFu, ow);
@@ -1016,28 +1019,26 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
         __syncthreads();
         if (r.warp == 0) {
             for (int it = base; it < min(n_steps, base + kBatch); ++it) {
-                const Pair next = at_a + Pair{sm->step_a[it - base].x, sm->step_a[it - base].y};
-                const unsigned next_t = at_t + sm->step_t[it - base];
-                const Pair c0 = kept(at_a, at_t);
-                if (c0 < kept(next, next_t) && !(target < c0)) {
+                const Pair here = {sm->step_a[it - base].x, sm->step_a[it - base].y};
+                const unsigned here_t = sm->step_t[it - base];
+                if ((here.h > 0.f || (here_t && at_t < ties)) && !(target < kept(at_a, at_t))) {
                     best = it;
                     best_a = at_a;
                     best_t = at_t;
                 }
-                at_a = next;
-                at_t = next_t;
+                at_a = at_a + here;
+                at_t += here_t;
             }
         }
     }
-    if (r.warp != 0 || best < 0) return;
+    if (r.warp != 0) return;
 
     // ---- the last lane, and in it the last token, whose kept weight begins at or before the target and is not nothing
     lane_sums(best, z, key, sa, st);
     Pair ca = best_a + lanes_below(sa, r.lane);
     unsigned ct = best_t + lanes_below(st, r.lane);
-    const Pair c0 = kept(ca, ct), c1 = kept(ca + sa, ct + st);
-    const unsigned may = __ballot_sync(0xffffffffu, c0 < c1 && !(target < c0));
-    const int who = may ? 31 - __clz(may) : 0;
+    const unsigned may = __ballot_sync(0xffffffffu, (sa.h > 0.f || (st && ct < ties)) && !(target < kept(ca, ct)));
+    const int who = 31 - __clz(may);
     int token = -1;
     float picked = m;
 #pragma unroll
@@ -1046,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
         const float2 v = weights2(g, make_float2(z[i], z[i + 1]), vl);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const bool takes = key[i + j] > keep || (key[i + j] == keep && ct < ties);
+            const bool takes = (key[i + j] > keep && (j ? v.y : v.x) > 0.f) || (key[i + j] == keep && ct < ties);
             if (takes && (token < 0 || !(target < kept(ca, ct)))) {
                 token = (int)first + (list ? sm->list_at[ow][(best * 32 + r.lane) * kPer + i + j] : r.token(a0 + best * 32 + r.lane, i + j));
                 picked = z[i + j];
