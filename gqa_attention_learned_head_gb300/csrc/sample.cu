@@ -1034,6 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
     if (r.warp != 0) return;
 
     // ---- the last lane, and in it the last token, whose kept weight begins at or before the target and is not nothing
+    const Pair wm = weight1(g, m);  // (all lanes)
     lane_sums(best, z, key, sa, st);
     Pair ca = best_a + lanes_below(sa, r.lane);
     unsigned ct = best_t + lanes_below(st, r.lane);
@@ -1058,7 +1059,7 @@ __global__ void __launch_bounds__(kThreads, 3) sample_kernel(const SampleArgs a)
     }
     if (r.lane == who) {
         a.out_tokens[row] = token;
-        if (a.out_logprobs) a.out_logprobs[row] = (float)(((double)picked - (double)m) / (double)t - (log(value(Z)) + short_of(g, m, t)));
+        if (a.out_logprobs) a.out_logprobs[row] = (float)(((double)picked - (double)m) / (double)t - log(value(Z) / value(wm)));
     }
 }
 

@@ -40,11 +40,6 @@ SINKATTN_HD RowScale row_scale(float m, float t) {
     g.least = (near ? y : 0.f) - kFloor;
     return g;
 }
-// ln of what the row's weights are short of e^((z - m) / t): add it to the logarithm of their sum.
-SINKATTN_HD double short_of(const RowScale& g, float m, float t) {
-    return g.ref == 0.f ? g.base * 0.69314718055994530942 - (double)m / (double)t : 0.0;
-}
-
 // One number at a time (on the GPU: two, sample.cu).
 struct OneByOne {
     using F = float;

@@ -56,3 +56,20 @@ def test_tokens_without_weight_between(S, dtype):
     low[:, 4000] = 3.0
     token, logprob = S.sinkattn_sample(low, u[[0, 4]], top_k=torch.full((2,), 50, dtype=torch.int32, device="cuda"))
     assert token.tolist() == [4000, 4000] and logprob.abs().max() <= 2.0**-28
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_a_sure_token_has_log_probability_zero(S, dtype):
+    """The only kept token, whatever the size of its logit and the temperature, by each filter and by itself."""
+    logits = torch.full((8, 999), -torch.inf, dtype=dtype, device="cuda")
+    logits[:, 500] = torch.tensor([3.0, -7.25, 0.3, 1e-4, 900.0, -31000.0, 0.0, 17.0]).to(dtype).cuda()
+    u = torch.rand(8, device="cuda")
+    t = torch.tensor([1.0, 0.7, 2.3, 0.01, 0.1, 1e-3, 5.0, 0.33], device="cuda")
+    for more in (False, True):
+        if more:
+            logits[:, 100:400] = (logits[:, 500:501].float() - 90 * t[:, None] - 0.02 * logits[:, 500:501].float().abs()).to(dtype)  # next to nothing
+        p, q = torch.full((8,), 0.5, device="cuda"), torch.full((8,), 0.5, device="cuda")
+        for kw in ((dict(top_p=p), dict(min_p=q), dict(top_k=torch.ones(8, dtype=torch.int32, device="cuda"))) if more else ({}, dict(top_p=p))):
+            token, logprob = S.sinkattn_sample(logits, u, t, **kw)
+            assert S.sinkattn_get_error() == 0
+            assert token.tolist() == [500] * 8 and not logprob.any(), kw

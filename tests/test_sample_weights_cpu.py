@@ -18,7 +18,7 @@ static const float roots[32][2] = SINKATTN_ROOTS;
 
 extern "C" void weights(const float* z, int n, float m, float t, float* out, double* row) {
     const RowScale g = row_scale(m, t);
-    row[0] = g.ref, row[1] = g.base, row[2] = short_of(g, m, t);
+    row[0] = g.ref, row[1] = g.base;
     for (int i = 0; i < n; ++i) {
         float y, k, r, h, l;
         split_power<OneByOne>(g, z[i], y, k, r);
@@ -42,16 +42,17 @@ def host(tmp_path_factory):
 def check(host, z, m, t):
     """z float32 logits up to m."""
     z = np.ascontiguousarray(z, dtype=np.float32)
-    out, row = np.zeros((len(z), 2), np.float32), np.zeros(3)
+    out, row = np.zeros((len(z), 2), np.float32), np.zeros(2)
     host.weights(at(z), len(z), np.ctypeslib.ctypes.c_float(m), np.ctypeslib.ctypes.c_float(t), at(out), at(row))
     m, t = np.longdouble(np.float32(m)), np.longdouble(np.float32(t))
     wide = out.astype(np.longdouble).sum(-1)
-    x = (z.astype(np.longdouble) - m) / t  # the definition: e^x, and what the row's weights are short of it
-    want = np.exp(x - np.longdouble(row[2]))
+    x = (z.astype(np.longdouble) - m) / t
+    with np.errstate(over="ignore"):
+        want = np.exp2((z.astype(np.longdouble) - np.longdouble(row[0])) / t / np.log(np.longdouble(2)) - np.longdouble(row[1]))
     has = x > -109 * np.log(np.longdouble(2))
     off = np.abs(wide - want)[has] / want[has]
-    # (short_of is rounded to 64 bits at a size of up to 4096 ln 2: 2^-41)
-    assert off.max() <= BOUND + 2.0**-41, float(np.log2(off.max()))
+    assert off.max() <= BOUND, float(np.log2(off.max()))
+    assert row[0] in (0.0, m) and 1 - 2.0**-11 <= wide[np.argmax(z)] < 2 + 2.0**-11  # (y is rounded before it gives the base)
     assert np.all(wide[x < -112 * np.log(np.longdouble(2))] == 0)
     assert np.all(np.abs(out[:, 1]) <= 2.0**-24 * out[:, 0])
     return off
@@ -91,6 +92,6 @@ def test_masked_and_far_logits(host):
 
 def test_one_temperature_for_all(host):
     """An infinite one: all finite logits weigh the same."""
-    out, row, z = np.zeros((4, 2), np.float32), np.zeros(3), np.array([3e38, 1.0, -3e38, -np.inf], np.float32)
+    out, row, z = np.zeros((4, 2), np.float32), np.zeros(2), np.array([3e38, 1.0, -3e38, -np.inf], np.float32)
     host.weights(at(z), 4, np.ctypeslib.ctypes.c_float(3e38), np.ctypeslib.ctypes.c_float(np.inf), at(out), at(row))
-    assert out[:3, 0].tolist() == [1.0] * 3 and out[3, 0] == 0 and not out[:, 1].any() and row[2] == 0
+    assert out[:3, 0].tolist() == [1.0] * 3 and out[3, 0] == 0 and not out[:, 1].any() and row[1] == 0
