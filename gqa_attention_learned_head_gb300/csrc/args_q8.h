@@ -7,8 +7,8 @@
 namespace sinkattn {
 
 // Exponents that a scale 2^e may have, and the largest code (e4m3).  2^40 x 448 is 4.9e14; the step at the least scale is 2^-49.
-// The range is this narrow on purpose: the spread of the scales of one sequence's value pages stays under 2^80, so that a softmax
-// sum held in 32 bits relative to one of them loses nothing that its largest term would not (decode_q8.cu).
+// The range is this narrow on purpose: value scales of one sequence are at most 2^80 apart, so that sums of weighted values relative to
+// any one of them stay within 32 bits (decode_q8.cu).
 constexpr int kScaleExpMin = -40, kScaleExpMax = 40;
 constexpr int kScaleBias = 127;  // a scale's byte is its exponent + 127 (E8M0)
 

@@ -16,21 +16,26 @@
 //  * V^T needs pairs of tokens in one register: four tokens' 8 dimensions are read with 8-byte loads and interleaved with byte
 //    permutes before they are converted.  Which token stands in which row of the score tile is free too: token_of() puts the pairs of
 //    K loads on different banks, and half of the V loads.
-//  * The weights in P V carry the value scale: w_j = 2^(x_j + ev(j) - R), x the scores in base 2, R a running bound of x + ev (raised,
-//    and O scaled down, only when a page exceeds it by more than kSlack).  They are held in f16, whose 11 bits round less than the
-//    bf16 output; kLift keeps w above f16's subnormals down to 2^-25 of the largest.  The sum of e^x is kept relative to the same R as
-//    sum w_j 2^-ev(j); exponents within -40..40 keep it inside 32 bits.  The sink joins when a piece ends, by its logarithm.
+//  * The value scale goes into the weights where it is within 2^2 of the scale 2^eo that a warp's accumulators have:
+//    w_j = 2^(x_j - R + ev(j) - eo), x the scores in base 2, R a running bound of x (raised, and O scaled down, only when a page exceeds
+//    it by more than kSlack).  They are held in f16, whose 11 bits round less than the bf16 output; kLift keeps w above f16's
+//    subnormals down to 2^-21 of the row's largest, and off by at most 2^-32 of it below.  A page further off gives the accumulators its
+//    own scale first (a power of two: exact).  Where its scale is more than 2^kSpread above another's, what its weights lose below
+//    2^-21 could outweigh the others: it takes them relative to its own largest, and its products are joined in 32 bits.  So one
+//    large value neither hides the other pages' dimensions nor is lost at a low score.  The sum of the weights is
+//    kept relative to R, without scales.  The sink joins when a piece ends, by its logarithm.
 //
 //  * Two pages are taken together: their bounds are compared before they are reduced over the lanes (only where one exceeds R does
 //    any shuffle run), and one turn of the loop waits, refills and branches for both.
 //
-// 2 x (64 + 1/16) bytes a token and KV head, 1/16 of it scales.  Measured (GB300): 4 x 131072 tokens 98 us, 5.5 TB/s = 81% of the
-// copy rate; 32 requests of 512 to 4096 tokens 30 us; one of 128 tokens 5.4.  What bounds the long case is no longer HBM alone: with half the
+// 2 x (64 + 1/16) bytes a token and KV head, 1/16 of it scales.  Measured (GB300): 4 x 131072 tokens 101 us, 5.3 TB/s = 79% of the
+// copy rate; 32 requests of 512 to 4096 tokens 31 us; one of 128 tokens 5.4.  What bounds the long case is no longer HBM alone: with half the
 // bytes a page, the same instructions a page take half of all issue slots, most of the rest waiting on the instruction before
 // (four warps a scheduler at 128 registers).  One page at a time: 118 us; two, with branches
 // for short and missing pages among their instructions: 105.  Products of codes with codes (the query as the sum
 // of two codes), which need no conversion of K: 120 us against 105, the fp8 form of mma.sync being no faster and K's conversions no longer
-// hidden.  Rings of 5 or 6 stages: 132, 121 us (fewer CTAs an SM); shares of at least 64 pages instead of 32: no change.
+// hidden.  Rings of 5 or 6 stages: 132, 121 us (fewer CTAs an SM); shares of at least 64 pages instead of 32: no change.  Weights with
+// all of the value scale in them, relative to a bound of x + ev, took 98 us and lost pages 2^25 and more below the largest scale.
 #include <type_traits>
 
 #include "args_merge.h"
@@ -57,8 +62,10 @@ constexpr int kStageBytes = 2 * kSliceBytes;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_huge_valf();
-constexpr float kLift = 11.f;  // weights are 2^kLift times their size, at most 2^(kLift + kSlack) = 2^15 < 65504
+constexpr float kLift = 9.f;  // weights are 2^kLift times their size, at most 2^(kLift + kSlack + kWindow) = 2^15 < 65504
 constexpr float kSlack = 4.f;
+constexpr int kWindow = 2;    // value exponents this near to the accumulators' go into the weights
+constexpr int kSpread = 6;    // pages of value exponents further than this above another's take weights relative to their own largest
 
 // The token of a page that row r of its score tile holds (r + 8: the same + 8).
 __device__ __forceinline__ int token_of(int r) { return (int)(0x65742130u >> (4 * r)) & 7; }
@@ -74,7 +81,8 @@ struct SmemLayout {
     static constexpr size_t cmb_md = cmb_o + 2 * size_t(kWarps) * kHeads * kHeadDim * 4;       // [2][warps][heads] R, d
     static constexpr size_t slot = cmb_md + 2 * size_t(kWarps) * kHeads * 8;                   // [2] arrivals, [2] generation
     static constexpr size_t scan = slot + 4 * 4;                                               // [kWarps] scan scratch
-    static constexpr size_t prefix = scan + kWarps * 4;
+    static constexpr size_t least = scan + kWarps * 4;                                         // [kWarps] least value exponents
+    static constexpr size_t prefix = least + kWarps * 4;
     static constexpr size_t fixed = prefix + 128 /* alignment slack */;
 };
 
@@ -285,7 +293,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
     const int gq = lane >> 2, tq = lane & 3;  // mma fragment coordinates
     const int tok0 = token_of(gq);            // rows gq, gq + 8 of the score tile: tokens tok0, tok0 + 8
     const int vt0 = token_of(2 * tq), vt1 = token_of(2 * tq + 1);
-    float O[4][NT][4];        // [dims 8 gq + 2 mt, + 1][heads 2 tq, 2 tq + 1], times 2^(kLift - R)
+    float O[4][NT][4];        // [dims 8 gq + 2 mt, + 1][heads 2 tq, 2 tq + 1], times 2^(kLift - R - eo)
+    int eo = kScaleBias;      // the value exponent of O, as a scale's byte
+    volatile int* const least = reinterpret_cast<int*>(sm + L::least) + warp;  // (at most) the least one of the piece's pages so far
     float R[NT][2], d[NT][2];
     int consumed = 0;
     bool failed = false;  // a wait gave up: skip all further work, keep the barriers
@@ -370,17 +380,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
             }
             const uint32_t word[2] = {my_meta[s0], two ? my_meta[s1] : 0u};
             uint8_t* const st[2] = {my_ring + s0 * kStageBytes, my_ring + s1 * kStageBytes};
+            if (t == 0) {
+                eo = word[0] ? (int)(word[0] >> 16) : kScaleBias;
+                *least = eo - kWindow;
+            }
+            const int up[2] = {(int)(word[0] >> 16) - eo, (int)(word[1] >> 16) - eo};
+            const bool calm = (unsigned)(up[0] + kWindow) <= 2u * kWindow && (unsigned)(up[1] + kWindow) <= 2u * kWindow;
             auto valid_of = [&](int j) { return word[j] == 0 ? 0 : min(kPageSize, cur.kv_len - cp.page(warp, t + j) * kPageSize); };
-            // (two whole pages, the usual case, without a branch, so that the instructions of both interleave)
+            // (two whole pages of like value scales, the usual case, without a branch, so that the instructions of both interleave)
             auto pages = [&](auto full) {
                 constexpr bool kFull = decltype(full)::value;
-                int ev[2];
                 float x[2][NT][4], top[NT][2];
     #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) top[nt][0] = top[nt][1] = kNegInf;
     #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    ev[j] = (int)(word[j] >> 16) - kScaleBias;
                     if (!kFull && j == 1 && !two) {
     #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -413,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                         for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[nt], af, qf[nt][kk][0], qf[nt][kk][1]);
                     }
                     // base-2 scores; this thread holds tokens tok0, tok0 + 8 and heads 2 tq, 2 tq + 1
-                    const float kf = __uint_as_float(word[j] << 23), evf = (float)ev[j];
+                    const float kf = __uint_as_float(word[j] << 23);
     #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         // (kf first: the product of the two factors may leave f32's range where the score does not)
@@ -425,7 +439,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                                 if (tok0 + (e >= 2 ? 8 : 0) >= valid) x[j][nt][e] = kNegInf;
                         }
     #pragma unroll
-                        for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(x[j][nt][e], x[j][nt][2 + e]) + evf);
+                        for (int e = 0; e < 2; ++e) top[nt][e] = fmaxf(top[nt][e], fmaxf(x[j][nt][e], x[j][nt][2 + e]));
                     }
                 }
 
@@ -463,17 +477,50 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                     const uint2 v1 = *reinterpret_cast<const uint2*>(vb + vt1 * kHeadDim);
                     const uint2 v2 = *reinterpret_cast<const uint2*>(vb + (vt0 + 8) * kHeadDim);
                     const uint2 v3 = *reinterpret_cast<const uint2*>(vb + (vt1 + 8) * kHeadDim);
-                    const float vinv = q8::power(-ev[j]), evl = (float)ev[j] + kLift;
+                    // the weights' bound and the size of the page's products, for each head
+                    float bound[NT][2], size[NT][2];
+                    const int byte = word[j] ? (int)(word[j] >> 16) : eo;  // (a page that is not there counts for nothing)
+                    const bool own = !kFull && byte > *least + kSpread;
+                    if (own) {  // weights relative to the page's own largest; products joined in 32 bits
+    #pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+    #pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float m = fmaxf(x[j][nt][e], x[j][nt][2 + e]);
+    #pragma unroll
+                                for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                                bound[nt][e] = m;
+                                size[nt][e] = m == kNegInf ? 0.f : fast_exp2(m - R[nt][e]);
+                            }
+                    } else {
+                        if (!kFull && (unsigned)(byte - eo + kWindow) > 2u * kWindow) {  // O takes the page's value scale
+                            const float f = q8::power(eo - byte);
+    #pragma unroll
+                            for (int mt = 0; mt < 4; ++mt)
+    #pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+    #pragma unroll
+                                    for (int e = 0; e < 4; ++e) O[mt][nt][e] *= f;
+                            eo = byte;
+                            *least = min(*least, eo - kWindow);
+                        }
+    #pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+    #pragma unroll
+                            for (int e = 0; e < 2; ++e) bound[nt][e] = R[nt][e];
+                    }
+                    const int lift = kFull ? up[j] : own ? 0 : byte - eo;
+                    const float vinv = q8::power(-lift), evl = (float)lift + kLift;
                     uint32_t pb[NT][2];
     #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        // (R = -inf: no key seen yet, and none here: every x is -inf)
-                        const float off0 = R[nt][0] == kNegInf ? 0.f : evl - R[nt][0];
-                        const float off1 = R[nt][1] == kNegInf ? 0.f : evl - R[nt][1];
+                        // (a bound of -inf: no key seen yet, and none here: every x is -inf)
+                        const float off0 = bound[nt][0] == kNegInf ? 0.f : evl - bound[nt][0];
+                        const float off1 = bound[nt][1] == kNegInf ? 0.f : evl - bound[nt][1];
                         const float p0 = fast_exp2(x[j][nt][0] + off0), p2 = fast_exp2(x[j][nt][2] + off0);
                         const float p1 = fast_exp2(x[j][nt][1] + off1), p3 = fast_exp2(x[j][nt][3] + off1);
-                        d[nt][0] += (p0 + p2) * vinv;
-                        d[nt][1] += (p1 + p3) * vinv;
+                        d[nt][0] += (p0 + p2) * (own ? size[nt][0] : vinv);
+                        d[nt][1] += (p1 + p3) * (own ? size[nt][1] : vinv);
                         pb[nt][0] = movmatrix_trans(pack_f16(p0, p1));  // rows 0..7  -> B rows k = 2tq, 2tq+1
                         pb[nt][1] = movmatrix_trans(pack_f16(p2, p3));  // rows 8..15
                     }
@@ -487,13 +534,29 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                             const uint32_t lo = __byte_perm(a0, a1, sel), hi = __byte_perm(a2, a3, sel);
                             const uint32_t af[4] = {q8::f16x2_of(lo), q8::f16x2_of_high(lo), q8::f16x2_of(hi), q8::f16x2_of_high(hi)};
     #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(O[2 * h + i][nt], af, pb[nt][0], pb[nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float (&o)[4] = O[2 * h + i][nt];
+                                if (own) {
+                                    const float f = q8::power(byte - eo);
+                                    float part[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16_16816(part, af, pb[nt][0], pb[nt][1]);
+    #pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[e] += part[e] * f * size[nt][e & 1];
+                                } else {
+                                    mma_f16_16816(o, af, pb[nt][0], pb[nt][1]);
+                                }
+                            }
                         }
                     }
                 }
             };
-            if (two && valid_of(0) == kPageSize && valid_of(1) == kPageSize) pages(std::true_type{});
-            else pages(std::false_type{});
+            if (calm && two && valid_of(0) == kPageSize && valid_of(1) == kPageSize) {
+                pages(std::true_type{});
+            } else {
+                if (word[0]) *least = min(*least, (int)(word[0] >> 16));
+                if (word[1]) *least = min(*least, (int)(word[1] >> 16));
+                pages(std::false_type{});
+            }
 
             // release the stages and refill them
             fence_proxy_async_smem();
@@ -511,6 +574,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) d[nt][e] += __shfl_xor_sync(0xffffffffu, d[nt][e], o);
 
+        const float unit = q8::power(eo - kScaleBias);  // (of a piece without pages: O is 0)
         const long long slot = cta + seg;  // partial slot of this piece
         if (!cp.split()) {
             if (cnt > 0) {
@@ -524,7 +588,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                         const float dt = d[nt][e];
                         const float keys = dt > 0.f ? R[nt][e] - kLift + log2f(dt) : (dt == 0.f ? kNegInf : dt);
                         const float all = first ? log2_sum(keys, __ldg(&a.sinks[cp.g * G + h]) * kLog2e) : keys;
-                        const float f = dt == 0.f ? 0.f : exp2f(keys - all) / dt;
+                        const float f = dt == 0.f ? 0.f : exp2f(keys - all) / dt * unit;
                         float v[8];
 #pragma unroll
                         for (int mt = 0; mt < 4; ++mt) {
@@ -568,8 +632,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3) decode_q8_kernel
                 for (int e = 0; e < 2; ++e) {
                     const int h = nt * 8 + 2 * tq + e;
                     float4* dst = reinterpret_cast<float4*>(co + (warp * L::kHeads + h) * kHeadDim + 8 * gq);
-                    dst[0] = make_float4(O[0][nt][e], O[0][nt][2 + e], O[1][nt][e], O[1][nt][2 + e]);
-                    dst[1] = make_float4(O[2][nt][e], O[2][nt][2 + e], O[3][nt][e], O[3][nt][2 + e]);
+                    dst[0] = make_float4(O[0][nt][e] * unit, O[0][nt][2 + e] * unit, O[1][nt][e] * unit, O[1][nt][2 + e] * unit);
+                    dst[1] = make_float4(O[2][nt][e] * unit, O[2][nt][2 + e] * unit, O[3][nt][e] * unit, O[3][nt][2 + e] * unit);
                     if (lane < 4) {
                         cmd[(warp * L::kHeads + h) * 2 + 0] = R[nt][e];
                         cmd[(warp * L::kHeads + h) * 2 + 1] = d[nt][e];

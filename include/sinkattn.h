@@ -680,7 +680,9 @@ size_t sinkattn_decode_q8_workspace_size(const sinkattn_decode_dims_t *dims);
 
 /*
  * sinkattn_decode over an 8-bit cache.  The queries and weights are multiplied with the codes in f16 (11 bits), sums
- * are held in 32 bits.  Arguments, workspace rules and errors are those of sinkattn_decode, and kv_scales.
+ * are held in 32 bits.  Weights keep their 11 bits down to 2^-21 of a row's largest and are off by at most 2^-32 of it
+ * below; those of a page whose values' scale is more than 2^6 above another's are taken relative to the page's own
+ * largest.  Arguments, workspace rules and errors are those of sinkattn_decode, and kv_scales.
  */
 sinkattn_status_t sinkattn_decode_q8(const void *q, const void *k_pages, const void *v_pages,
                                      const uint8_t *kv_scales, const int32_t *page_table, const int32_t *kv_lens,
