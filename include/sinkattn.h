@@ -630,8 +630,9 @@ sinkattn_status_t sinkattn_decode_beams(const void *q, const void *k_pages, cons
  *   k, v, cu_seqlens, start_pos, page_table: as sinkattn_kv_append
  *   k_pages, v_pages, kv_scales: written in place; 16-byte, 16-byte and 2-byte aligned
  *
- * The pages written must be held by one sequence only.  Bad page ids, positions and packings are reported as in
- * sinkattn_kv_append and skip their tokens.  A NaN or infinity is held as a NaN (its page's scale goes by the
+ * The pages written must be held by one sequence only.  Bad page ids and positions are reported as in
+ * sinkattn_kv_append and skip their tokens.  A packing that is not 0 <= cu_seqlens[n] <= cu_seqlens[n + 1] <= T raises
+ * SINKATTN_ERR_BAD_LENGTH; tokens of any sequence may then be left out, a page at a time.  A NaN or infinity is held as a NaN (its page's scale goes by the
  * finite values), a value beyond 448 * 2^40 as that, and both raise SINKATTN_ERR_BAD_VALUE.
  */
 sinkattn_status_t sinkattn_kv_append_q8(const void *k, const void *v, const int32_t *cu_seqlens,
@@ -641,9 +642,8 @@ sinkattn_status_t sinkattn_kv_append_q8(const void *k, const void *v, const int3
 
 /*
  * sinkattn_qkv_prologue into an 8-bit cache: bias and rotation in 32 bits, q rounded to bf16, keys and values
- * rounded once, from 32 bits to 8, as sinkattn_kv_append_q8 does.  Arguments as those two calls'.  With a packing
- * that is not 0 <= cu_seqlens[n] <= cu_seqlens[n + 1] <= T (SINKATTN_ERR_BAD_LENGTH), q_out holds only the tokens
- * of the sequences that are.
+ * rounded once, from 32 bits to 8, as sinkattn_kv_append_q8 does.  Arguments as those two calls'.  Where a bad packing
+ * leaves tokens out of the pages, their rows of q_out are not written either.
  */
 sinkattn_status_t sinkattn_qkv_prologue_q8(const void *qkv, const void *bias, const int32_t *cu_seqlens,
                                            const int32_t *start_pos, const int32_t *page_table,
