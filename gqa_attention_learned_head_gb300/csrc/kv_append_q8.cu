@@ -19,7 +19,8 @@
 //
 // Measured (GB300, 64 query and 8 KV heads, bias, rotation): eight chunks of 256 to 2048 tokens 39.6 us, 4.5 TB/s = 66% of the copy
 // rate (CTAs of 8 warps 42.9; fewer registers, and with them more warps an SM, 51 to 61: what counts is the loads a warp has in flight,
-// the next heads' while these are computed); 128 single tokens 4.3 us, the latency of one kernel.
+// the next heads' while these are computed); 128 single tokens 4.4 us, the latency of one kernel.  Ready keys and values: 8.5 us (9113
+// tokens, out of L2), 3.0 us.
 #include "args_q8.h"
 #include "ptx.cuh"
 #include "q8.cuh"
@@ -28,8 +29,9 @@ namespace sinkattn {
 namespace {
 
 constexpr int kWarps = 4;
-// Up to so many units (two for each of 152 SMs) their heads are dealt to two CTAs each.  Measured: 128 single tokens 4.75 -> 4.3 us;
-// eight chunks, 590 units, 39.6 -> 43 us.
+// Up to so many units (two for each of 152 SMs) their heads are dealt to two CTAs each.  Measured with one and with two, 64 query and 8 KV
+// heads: chunks, 144 units 28.7 and 18.9 us, 306 units 31.9 and 24.4, 336 units 32.5 and 37.2, 516 units 37.4 and 40.9; single
+// tokens (most units of which are idle) 249 units 4.8 and 4.3, 497 units 5.3 and 4.6, 621 units 5.4 and 5.8.
 constexpr long long kFewUnits = 304;
 constexpr float kInf = __builtin_huge_valf();
 

@@ -170,7 +170,7 @@ cudaError_t widen_q8_launch(const WidenQ8Args& a, cudaStream_t stream) {
     static thread_local bool done[64] = {};
     const size_t smem = (size_t)(a.N + 1) * sizeof(int);
     if (smem > 40000 && (e = allow_all_smem(reinterpret_cast<const void*>(widen_q8_kernel), dev, done)) != cudaSuccess) return e;
-    // as many CTAs as run at once, fewer where the tables cannot hold a page for each warp
+    // eight CTAs an SM (six run at once, at 40 registers), fewer where the tables cannot hold a page for each warp
     const long long most = ((long long)a.N * a.max_pages * a.Hkv + kWarps - 1) / kWarps;
     const long long resident = (long long)sms * (smem > 24000 ? 3 : 8);
     cudaLaunchAttribute attr[1];

@@ -23,11 +23,13 @@
 //    in one of them.  Kept ties need no list: the kept weights up to a token are (those with z > z*) + w(z*) min(r, number of
 //    z = z* so far).
 //
-// Bound by instructions, not by HBM, which the row's one reading leaves idle 95% of the time.  Measured (GB300): 256 rows of 50021
-// f32, settings of their own, 96 us (7.6 of reading): a CTA takes 27 us (load 2.3, maximum 2, first bins 5, list and sort 8 to
-// 12, sums 2.5, the rest waits of eight exchanges within the cluster), 1024 CTAs in three waves; 64 rows of 200000 bf16, top-p of a flat
-// distribution, 93 us (3.8): weights of every token twice the 30000 clocks that one sum over a CTA's 25000 tokens takes,
-// with three CTAs on an SM.  One row of 32000: 15 us, latency.  Three CTAs an SM (80 registers) instead of two: 10% faster.
+// Bound by neither HBM, which the row's one reading leaves idle 93% of the time and more, nor by one unit of the SM: at 80 registers and
+// 74 KB three CTAs share an SM, whose issue slots are 35 to 37% busy; the rest are waits, on the instruction before, at barriers and on
+// the cluster.  Measured (GB300): 256 rows of 50021 f32, settings of their own, 96 us (7.6 of reading): a CTA takes 27 us (load 2.3, maximum 2,
+// first bins 5, list and sort 8 to 12, sums 2.5, the rest waits of eight exchanges within the cluster), 1024 CTAs in three waves; 64 rows
+// of 200000 bf16, top-p of a flat distribution, 93 us (3.8): weights of every token twice, two waves.  One row of 32000: 15 to 19 us by its
+// settings, latency.  f32 rows of 200000 leave one CTA on an SM (a chunk takes 100 KB): 64 of them 88 us without filters, 226 with top-p.
+// Three CTAs an SM (80 registers) instead of two: 10% faster.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1073,8 +1075,9 @@ cudaError_t launch(SampleArgs a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     static thread_local bool done[64] = {};
     if ((e = allow_all_smem(reinterpret_cast<const void*>(sample_kernel<T>), dev, done)) != cudaSuccess) return e;
-    // CTAs a row: as many as it takes to keep a chunk within a quarter of an SM's shared memory (four CTAs an SM hide each other's
-    // waits), more while the rows leave SMs without work and a chunk has a few thousand tokens left
+    // CTAs a row: as many as it takes to keep a chunk within what lets three CTAs share an SM (52 KB beside 22 KB of Smem; the registers
+    // allow three, which hide each other's waits), more while the rows leave SMs without work and a chunk has a few thousand tokens left.
+    // Rows that eight such chunks cannot hold have larger ones, and fewer CTAs an SM.
     const size_t room = 52 * 1024;
     int size = 1;
     while (size < kMaxCluster && (size_t)a.V * sizeof(T) > room * size) size *= 2;

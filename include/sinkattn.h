@@ -727,12 +727,11 @@ typedef struct {
  *          below it; at least one),
  *   min_p  of those the ones whose weight is at least min_p.
  * With Z the sum of the kept weights the token chosen is the first, in the order of the vocabulary, up to and
- * with which the kept weights sum to more than uniform * Z.  Weights are off by at most 2^-28.5
- * of themselves, equal logits' alike, and sums are held in 46 bits, so that the choice is that of exact arithmetic but for a chance of
- * about 1e-7 a row with 10^5 tokens of like weight and as many values; where few values are held by many tokens each (ties,
- * 16-bit logits) of about 1e-5 with 10^5 tokens of 50 values, and never more than 2^-29 times the number of kept tokens.
- * The blog posts describing the method
- * have no counterpart to this call.
+ * with which the kept weights sum to more than uniform * Z.  Weights are off by at most 2^-28.5 of themselves, equal
+ * logits' alike, and sums are held in 46 bits, so that the choice is that of exact arithmetic but for a chance of about
+ * 1e-7 a row with 10^5 tokens of like weight and as many values; where few values are held by many tokens each (ties,
+ * 16-bit logits) of about 1e-5 with 10^5 tokens of 50 values, and never more than 2^-29 times the number of kept
+ * tokens.  The blog posts describing the method have no counterpart to this call.
  *
  *   logits       [N, V]  f32, bf16 or f16; row n starts row_stride elements after row n - 1
  *   uniform      [N]     f32 in [0, 1)
